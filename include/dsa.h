@@ -373,6 +373,152 @@ dsa_status dsa_selftest_wait_timeout(int32_t limit_us, void* stream);
 dsa_status dsa_quantize_fp8(const void* x_bf16, int64_t rows, int32_t cols, uint8_t* codes, float* scale,
                             void* stream);
 
+/* ---- operators around the caches: norm, rotary positions, cache append, window attention ------- */
+
+/* Element type of the tensors of dsa_rmsnorm, dsa_rmsnorm_backward and dsa_rope. */
+typedef enum { DSA_BF16 = 0, DSA_F16 = 1, DSA_F32 = 2 } dsa_dtype;
+
+/* Which elements of a head's rotated dims r = 0 .. rot_dim-1 form pair i: (2i, 2i + 1) or (i, i + rot_dim/2). */
+typedef enum { DSA_ROPE_INTERLEAVED = 0, DSA_ROPE_HALF = 1 } dsa_rope_layout;
+
+/* Frequency scaling of dsa_rope_frequencies for contexts longer than the trained one. */
+typedef enum { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_NTK = 2, DSA_ROPE_YARN = 3 } dsa_rope_scaling;
+
+/* Columns that share one scale of dsa_rmsnorm's 8-bit output in its grouped form. */
+#define DSA_QUANT_GROUP 128
+
+/*
+ * Root-mean-square norm with the residual's addition and an optional 8-bit output (the step before
+ * the projections that make q, q_I, k_I and the latent; the pages take those projections as given).
+ * For each row r, in fp32 and rounded once at the end:
+ *   h = x[r,:] + residual[r,:]     (residual NULL: h = x)
+ *   rs = 1 / sqrt(mean(h^2) + eps),  v = h * rs * weight
+ *   residual_out[r,:] = h          (when not NULL)
+ *   y[r,:] = v                     (when not NULL)
+ *   codes[r*cols + c] = e4m3(v_c / s), s = amax |v| / 448 (1 where the maximum is 0), over the row
+ *     (group = 0: scale [rows]) or over each DSA_QUANT_GROUP columns (group = DSA_QUANT_GROUP:
+ *     scale [rows, ceil(cols / 128)]), taken from the unrounded v, saturating at +-448.  NaN takes
+ *     no part in the maximum and encodes as NaN.  codes and scale come together (both or neither).
+ *   rstd[r] = rs                   (when not NULL; dsa_rmsnorm_backward reads it)
+ * x, residual, y and residual_out are [rows, cols] of `dtype` with row strides ld_* in elements
+ * (>= cols); weight [cols] of `dtype`; codes dense.  At least one of y and codes.  y or residual_out
+ * may be x or residual itself (same pointer and stride); no other overlap.  Any cols >= 1 and any
+ * element-aligned pointers and strides (16-byte aligned pointers with strides and cols that are
+ * multiples of 8 take the wide-load path).  rows == 0 is a no-op.
+ * DSA_ERR_INVALID_ARGUMENT: NULL or misaligned pointers, sizes or strides as above, group not 0 or
+ * DSA_QUANT_GROUP, eps negative or not finite, unknown dtype; DSA_ERR_UNSUPPORTED: rows > 2^31 - 1.
+ */
+dsa_status dsa_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual, const void* weight,
+                       int64_t rows, int32_t cols, int32_t dtype, float eps, void* y, int64_t ld_y,
+                       void* residual_out, int64_t ld_residual_out, uint8_t* codes, float* scale, int32_t group,
+                       float* rstd, void* stream);
+
+/*
+ * Backward of dsa_rmsnorm's y with respect to h and weight: with g = dy * weight,
+ *   dh[r,:] = rstd[r] * (g - h * rstd[r]^2 * mean(g * h)) + dresidual[r,:]   (dresidual may be NULL)
+ *   dw[c] = sum_r dy[r,c] * h[r,c] * rstd[r]
+ * h is the sum that was normalised (residual_out, or x without a residual), dresidual the gradient
+ * that reaches residual_out; dh is the gradient of x and of residual alike.  All [rows, cols] of
+ * `dtype` with row strides; weight [cols] of `dtype`, rstd [rows] and dw [cols] fp32.  Sums in fp32;
+ * dw is summed in a fixed order (a run repeats its bits).  dh may be dy or dresidual itself.
+ * workspace (device, 16-byte aligned): dsa_rmsnorm_backward_workspace_size(rows, cols) bytes, else
+ * DSA_ERR_WORKSPACE_TOO_SMALL.  rows == 0 sets dw to zero.  Other errors as dsa_rmsnorm.
+ */
+dsa_status dsa_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* weight,
+                                const float* rstd, const void* dresidual, int64_t ld_dresidual, int64_t rows,
+                                int32_t cols, int32_t dtype, void* dh, int64_t ld_dh, float* dw, void* workspace,
+                                size_t ws_bytes, void* stream);
+size_t dsa_rmsnorm_backward_workspace_size(int64_t rows, int32_t cols);
+
+/*
+ * Rotary positions on a part of each head (the 64 "rope" dims of q and of the latent; the indexer's
+ * q_I and k_I): for row r, head j and pair i of the dims [rot_offset, rot_offset + rot_dim), with
+ * angle = positions[r] * freqs[i] (radians, formed in fp64), c = mscale * cos, s = mscale * sin:
+ *   (a, b) -> (a c - b s, a s + b c);   transpose != 0: (a c + b s, b c - a s), the backward pass.
+ * The other dims are copied when out != x and left alone when out == x (same strides).  x and out
+ * are [rows, heads, dim] of `dtype` with row and head strides in elements (head stride >= dim;
+ * the row stride of one head at least dim); out either is x or overlaps it nowhere, and no two
+ * (row, head) pieces of out overlap.  positions [rows] int32 (any sign), freqs [rot_dim/2] fp64 on
+ * the device.  Computed in fp32, rounded once.
+ * rows == 0 or heads == 0 is a no-op.  DSA_ERR_INVALID_ARGUMENT: NULL or misaligned pointers,
+ * rot_dim odd or < 2, a range outside the head, strides too small, unknown layout or dtype, mscale
+ * not finite, out == x with other strides; DSA_ERR_UNSUPPORTED: rot_dim > 1024, or rows or
+ * heads * dim above 2^31 - 1.
+ */
+dsa_status dsa_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride, void* out, int64_t out_row_stride,
+                    int64_t out_head_stride, int64_t rows, int32_t heads, int32_t dim, int32_t rot_offset,
+                    int32_t rot_dim, int32_t layout, int32_t dtype, const int32_t* positions, const double* freqs,
+                    float mscale, int32_t transpose, void* stream);
+
+/*
+ * Frequencies for dsa_rope and dsa_cache_append (host only; freqs is a HOST array of rot_dim/2):
+ * f_i = theta^(-2i / rot_dim), then for a context `factor` (>= 1) times original_ctx
+ *   DSA_ROPE_PLAIN   f_i                         DSA_ROPE_LINEAR  f_i / factor
+ *   DSA_ROPE_NTK     theta * factor^(rot_dim / (rot_dim - 2)) in theta's place (rot_dim >= 4)
+ *   DSA_ROPE_YARN    f_i / factor * ramp_i + f_i * (1 - ramp_i), ramp_i = clamp((i - low) / (high - low), 0, 1),
+ *     low = max(floor(d(beta_fast)), 0), high = min(ceil(d(beta_slow)), rot_dim - 1) (high - low at
+ *     least 0.001), d(n) = rot_dim * ln(original_ctx / (2 pi n)) / (2 ln theta)
+ * (the published NTK-aware and YaRN methods).  *mscale receives 0.1 ln(factor) + 1 for YaRN, else 1.
+ * factor is read for LINEAR, NTK and YARN, the last three for YARN only.
+ * DSA_ERR_INVALID_ARGUMENT: NULL pointers, rot_dim odd or < 2, theta <= 1, or a value that is read
+ * and out of range (factor < 1, original_ctx <= 0, beta_slow <= 0, beta_fast < beta_slow, not finite).
+ */
+dsa_status dsa_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling, double factor, double original_ctx,
+                                double beta_fast, double beta_slow, double* freqs, float* mscale);
+
+/*
+ * Appends tokens to the latent cache and to the indexer-key cache, in one launch: row r is the
+ * token at position positions[r] of sequence seq[r] (seq NULL: sequence r).
+ *   latent row: kv[r, 0:512] RMS-normalised with kv_weight [512] and eps, kv[r, 512:576] rotated
+ *     (dsa_rope with `layout`), both in fp32, rounded once to bf16;
+ *   indexer key: key[r, :] with dims [key_rot_offset, key_rot_offset + 64) rotated (`key_layout`),
+ *     quantised as dsa_quantize_fp8 does a row (scale = amax / 448, from the unrounded values; 1
+ *     for an all-zero row).
+ * kv [rows, 576] and key [rows, d_I] are bf16 with row strides ld_*; freqs [32] fp64 (device).
+ * latent and keys describe the caches (contiguous or paged; the library writes data and scale):
+ * paged, position p of sequence b is row block_table[b, p/64] * 64 + p % 64; contiguous, row
+ * cu_seqlens[b] + p, which must lie before cu_seqlens[b+1].  context_lens is not read.  Either half may be
+ * left out: kv and latent NULL, or key and keys NULL.  A row with seq -1 is padding and skipped.
+ * A row whose sequence, position (>= max_seqlen) or block is out of range is skipped and sets
+ * DSA_ERR_DEVICE_CHECK.  Rows must name distinct (sequence, position) slots, and no two
+ * sequences share a page that is written: which row's values a slot named twice keeps is not defined.
+ * Slots that no row names are not touched.  rows == 0 is a no-op.
+ * DSA_ERR_INVALID_ARGUMENT: NULL pointers, kv not 16-byte aligned or ld_kv no multiple of 8, key not
+ * 4-byte aligned or ld_key odd, key_rot_offset odd or outside [0, d_I - 64], caches misaligned
+ * (latent data 16 bytes, key data 2), inconsistent sizes; DSA_ERR_UNSUPPORTED: d_I not 64 or 128,
+ * page size other than 64, rows > 2^31 - 1.
+ */
+dsa_status dsa_cache_append(const void* kv, int64_t ld_kv, const void* kv_weight, float eps, const void* key,
+                            int64_t ld_key, int32_t d_I, const int32_t* seq, const int32_t* positions, int64_t rows,
+                            int32_t B, const double* freqs, float mscale, int32_t layout, int32_t key_layout,
+                            int32_t key_rot_offset, const dsa_kv_desc* latent, const dsa_kv_desc* keys, void* stream);
+
+/*
+ * MLA attention (MQA mode, as dsa_sparse_mla_*) with a sliding window and sinks instead of a selection:
+ * the query at position t sees the keys s <= t with s > t - window (its window, itself included) or
+ * s < sinks (the first tokens of its sequence).  window >= 1, sinks >= 0; a window of at least the
+ * context gives dense causal attention.  out and lse as dsa_sparse_mla_prefill; a row without a
+ * visible key gets out = 0 and lse = -INFINITY.  Keys outside the window are not read, whatever
+ * they hold (NaN included).  The softmax sums are fp32, its probabilities bf16 in the product with the values.
+ *   prefill: latent contiguous, queries are the packed tokens [0, cu_seqlens[B]); rows of out and lse
+ *     behind the last sequence are left as they were.
+ *   decode: latent paged, one query per sequence at position ctx - 1, ctx = context_lens[b] clamped
+ *     to [0, latent->max_seqlen] (clamping sets DSA_ERR_DEVICE_CHECK).  The visible keys are split
+ *     over the GPU when the sequences alone do not fill it; the parts go to `workspace`
+ *     (256-byte aligned, dsa_window_mla_workspace_size bytes; may be NULL where that is 0) and are merged
+ *     by log-sum-exp.  Keys in blocks outside the pool are masked and set DSA_ERR_DEVICE_CHECK.
+ * Forward only, like every attention of this library.  1 <= H <= 128 (64-head tiles: small H costs as
+ * much as 128).  DSA_ERR_INVALID_ARGUMENT: as dsa_sparse_mla_*, window < 1, sinks < 0, sm_scale negative
+ * or not finite; DSA_ERR_UNSUPPORTED: H, the page size, or sizes beyond 2^31 - 1 rows.
+ */
+dsa_status dsa_window_mla_prefill(const void* q, const dsa_kv_desc* latent, int32_t B, int32_t H, int32_t window,
+                                  int32_t sinks, float sm_scale, void* out, float* lse, void* stream);
+dsa_status dsa_window_mla_decode(const void* q, const dsa_kv_desc* latent, int32_t B, int32_t H, int32_t window,
+                                 int32_t sinks, float sm_scale, void* out, float* lse, void* workspace,
+                                 size_t ws_bytes, void* stream);
+/* Workspace bytes of dsa_window_mla_decode (max_ctx = latent->max_seqlen; 0 when nothing is split). */
+size_t dsa_window_mla_workspace_size(int32_t B, int32_t H, int32_t window, int32_t sinks, int32_t max_ctx);
+
 #ifdef __cplusplus
 }
 #endif

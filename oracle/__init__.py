@@ -51,6 +51,10 @@ Parity status per function (what pins it, in ``tests/test_oracle_*.py``):
 * ``encode_e4m3`` / ``quantize_fp8_rows``: pinned (every finite code round-trips; midpoints
   between neighbouring values go to the even code; saturation and NaN; agreement with torch's
   float8_e4m3fn cast on random values; the per-row scale rule and its error bound).
+* ``cache_ops`` (``rmsnorm``, ``rmsnorm_backward``, ``rope``, ``rope_frequencies``, ``cache_rows``,
+  ``window_mla_token``): pinned (the library's float64 RMS norm and its autograd; rotations as
+  products of complex numbers, lengths kept, dot products a function of the distance, the
+  transpose as inverse; scaled frequencies' limits; a library's dense masked attention).
 * Agreement with DeepSeek's trained model: parity unpinned (no weights, no printed values).
 """
 
@@ -77,4 +81,14 @@ from .dsa_oracle import (  # noqa: F401
     decode_indexer_scores,
     dsa_prefill_rows,
     dsa_decode,
+)
+from .cache_ops import (  # noqa: F401
+    rmsnorm,
+    rmsnorm_backward,
+    row_scales,
+    rope,
+    rope_frequencies,
+    cache_rows,
+    window_positions,
+    window_mla_token,
 )

@@ -30,13 +30,26 @@ DSA_KV_CONTIGUOUS = 0
 DSA_KV_PAGED = 1
 DSA_MODE_PREFILL = 0
 DSA_MODE_DECODE = 1
+DSA_BF16 = 0
+DSA_F16 = 1
+DSA_F32 = 2
+DSA_ROPE_INTERLEAVED = 0
+DSA_ROPE_HALF = 1
+DSA_ROPE_PLAIN = 0
+DSA_ROPE_LINEAR = 1
+DSA_ROPE_NTK = 2
+DSA_ROPE_YARN = 3
+DSA_QUANT_GROUP = 128
 
 EXPORTED = ("dsa_indexer_scores", "dsa_indexer_topk", "dsa_topk", "dsa_sparse_mla_prefill", "dsa_sparse_mla_decode",
             "dsa_forward", "dsa_workspace_size", "dsa_status_string", "dsa_device_error",
             "dsa_sparse_mla_decode_noalloc", "dsa_quantize_fp8", "dsa_masked_mla_prefill",
             "dsa_indexer_topk_rows", "dsa_sparse_mla_prefill_rows", "dsa_attn_distribution", "dsa_indexer_kl",
             "dsa_selftest_wait_timeout", "dsa_row_partition", "dsa_indexer_topk_decode",
-            "dsa_decode_select_workspace_size", "dsa_attn_distribution_dense", "dsa_indexer_backward")
+            "dsa_decode_select_workspace_size", "dsa_attn_distribution_dense", "dsa_indexer_backward",
+            "dsa_rmsnorm", "dsa_rmsnorm_backward", "dsa_rmsnorm_backward_workspace_size", "dsa_rope",
+            "dsa_rope_frequencies", "dsa_cache_append", "dsa_window_mla_prefill", "dsa_window_mla_decode",
+            "dsa_window_mla_workspace_size")
 
 
 class KVDesc(ctypes.Structure):
@@ -107,6 +120,27 @@ _lib.dsa_attn_distribution_dense.argtypes = [_P, _DESC, _P, _I32, _I32, _I64, _I
 _lib.dsa_attn_distribution_dense.restype = _I32
 _lib.dsa_indexer_backward.argtypes = [_P, _P, _I32, _P, _DESC, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P]
 _lib.dsa_indexer_backward.restype = _I32
+_F64 = ctypes.c_double
+_lib.dsa_rmsnorm.argtypes = [_P, _I64, _P, _I64, _P, _I64, _I32, _I32, _F32, _P, _I64, _P, _I64, _P, _P, _I32, _P, _P]
+_lib.dsa_rmsnorm.restype = _I32
+_lib.dsa_rmsnorm_backward.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _I64, _I64, _I32, _I32, _P, _I64, _P, _P, _SZ, _P]
+_lib.dsa_rmsnorm_backward.restype = _I32
+_lib.dsa_rmsnorm_backward_workspace_size.argtypes = [_I64, _I32]
+_lib.dsa_rmsnorm_backward_workspace_size.restype = _SZ
+_lib.dsa_rope.argtypes = [_P, _I64, _I64, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _F32, _I32,
+                          _P]
+_lib.dsa_rope.restype = _I32
+_lib.dsa_rope_frequencies.argtypes = [_I32, _F64, _I32, _F64, _F64, _F64, _F64, _P, ctypes.POINTER(_F32)]
+_lib.dsa_rope_frequencies.restype = _I32
+_lib.dsa_cache_append.argtypes = [_P, _I64, _P, _F32, _P, _I64, _I32, _P, _P, _I64, _I32, _P, _F32, _I32, _I32, _I32,
+                                  _DESC, _DESC, _P]
+_lib.dsa_cache_append.restype = _I32
+_lib.dsa_window_mla_prefill.argtypes = [_P, _DESC, _I32, _I32, _I32, _I32, _F32, _P, _P, _P]
+_lib.dsa_window_mla_prefill.restype = _I32
+_lib.dsa_window_mla_decode.argtypes = [_P, _DESC, _I32, _I32, _I32, _I32, _F32, _P, _P, _P, _SZ, _P]
+_lib.dsa_window_mla_decode.restype = _I32
+_lib.dsa_window_mla_workspace_size.argtypes = [_I32, _I32, _I32, _I32, _I32]
+_lib.dsa_window_mla_workspace_size.restype = _SZ
 
 
 class DSAError(RuntimeError):
@@ -141,9 +175,10 @@ def _check(status, where):
 class Desc:
     """A dsa_kv_desc plus references to the tensors it points at."""
 
-    def __init__(self, struct: KVDesc, refs):
+    def __init__(self, struct: KVDesc, refs, batch=0):
         self.struct = struct
         self._refs = refs
+        self.batch = int(batch)  # sequences
 
     def ref(self):
         return ctypes.byref(self.struct)
@@ -155,7 +190,7 @@ def contiguous_desc(data, cu_seqlens, max_seqlen, scale=None) -> Desc:
                cu_seqlens=cu_seqlens.data_ptr(), block_table=None, context_lens=None,
                total_tokens=int(data.shape[0]), max_seqlen=int(max_seqlen), num_blocks=0, block_size=0,
                max_blocks_per_seq=0)
-    return Desc(s, (data, scale, cu_seqlens))
+    return Desc(s, (data, scale, cu_seqlens), cu_seqlens.shape[0] - 1)
 
 
 def paged_desc(data, block_table, context_lens, max_ctx, scale=None) -> Desc:
@@ -164,7 +199,7 @@ def paged_desc(data, block_table, context_lens, max_ctx, scale=None) -> Desc:
                cu_seqlens=None, block_table=block_table.data_ptr(), context_lens=context_lens.data_ptr(),
                total_tokens=0, max_seqlen=int(max_ctx), num_blocks=int(data.shape[0]),
                block_size=int(data.shape[1]), max_blocks_per_seq=int(block_table.shape[1]))
-    return Desc(s, (data, scale, block_table, context_lens))
+    return Desc(s, (data, scale, block_table, context_lens), block_table.shape[0])
 
 
 def dsa_quantize_fp8(x, codes, scale, stream=None):
@@ -333,3 +368,187 @@ def dsa_row_partition(L, k, parts, indexer_cost, mla_cost):
     _check(_lib.dsa_row_partition(int(L), int(k), int(parts), float(indexer_cost), float(mla_cost), out),
            "dsa_row_partition")
     return [int(x) for x in out]
+
+
+# ---- operators around the caches: norm, rotary positions, cache append, window attention ----------
+# These take tensors whose type, shape and strides the C ABI cannot see, so each is checked here
+# (ValueError); a tensor on another device than the current one is refused, because the stream the
+# work goes to is the current device's.
+
+_DTYPES = {torch.bfloat16: DSA_BF16, torch.float16: DSA_F16, torch.float32: DSA_F32}
+
+
+def _dense(where, name, t, dtype, shape):
+    """The address of a contiguous tensor of this type and shape on the current device (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{where}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the current "
+                         f"device, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def _strided(where, name, t, dtype, shape):
+    """(address, row stride) of a tensor of this type and shape whose last dimension is dense."""
+    if t is None:
+        return None, 0
+    if (t.dtype is not dtype or t.shape != shape or (t.stride(-1) != 1 and shape[-1] > 1)
+            or t.get_device() != torch.cuda.current_device()):
+        raise ValueError(f"{where}: {name} must be a {dtype} tensor of shape {tuple(shape)}, dense in its last dimension, "
+                         f"on the current device, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[-1])
+
+
+def _on_device(where, t, *dims):
+    """Type code of a floating tensor with one of these numbers of dimensions on a GPU."""
+    if t.get_device() < 0:
+        raise ValueError(f"{where}: tensors must be on a CUDA device, got {t.device}")
+    if t.dtype not in _DTYPES or t.dim() not in dims:
+        raise ValueError(f"{where}: expected a bf16, fp16 or fp32 tensor of {dims} dimensions, got {t.dtype} {tuple(t.shape)}")
+    return _DTYPES[t.dtype]
+
+
+def dsa_rmsnorm(x, weight, eps, y=None, residual=None, residual_out=None, codes=None, scale=None, rstd=None, stream=None):
+    """h = x + residual; y = h * rsqrt(mean(h^2) + eps) * weight, and/or its e4m3 codes [rows, cols]
+    (uint8) with scale [rows] (one per row) or [rows, ceil(cols / 128)] (one per 128 columns);
+    residual_out = h; rstd [rows] for the backward.  x, residual, y, residual_out: [rows, cols] of one
+    type (bf16, fp16, fp32), any row stride; y and residual_out may be x or residual."""
+    w = "dsa_rmsnorm"
+    dtype = _on_device(w, x, 2)
+    rows, cols = shape = tuple(x.shape)
+    xp, xl = _strided(w, "x", x, x.dtype, shape)
+    rp, rl = _strided(w, "residual", residual, x.dtype, shape)
+    yp, yl = _strided(w, "y", y, x.dtype, shape)
+    op, ol = _strided(w, "residual_out", residual_out, x.dtype, shape)
+    groups = -(-cols // DSA_QUANT_GROUP)
+    grouped = scale is not None and scale.dim() == 2
+    _check(_lib.dsa_rmsnorm(xp, xl, rp, rl, _dense(w, "weight", weight, x.dtype, (cols,)), rows, cols, dtype, float(eps), yp,
+                            yl, op, ol, _dense(w, "codes", codes, torch.uint8, shape),
+                            _dense(w, "scale", scale, torch.float32, (rows, groups) if grouped else (rows,)),
+                            DSA_QUANT_GROUP if grouped else 0, _dense(w, "rstd", rstd, torch.float32, (rows,)),
+                            _stream(stream)), w)
+    return y if y is not None else codes
+
+
+def dsa_rmsnorm_backward_workspace_size(rows, cols) -> int:
+    return int(_lib.dsa_rmsnorm_backward_workspace_size(int(rows), int(cols)))
+
+
+def dsa_rmsnorm_backward(dy, h, weight, rstd, dh, dw, workspace, dresidual=None, stream=None):
+    """Gradients of dsa_rmsnorm: dh [rows, cols] (of x and of residual; plus dresidual, the gradient
+    of residual_out) and dw [cols] fp32 from dy, h (residual_out, or x without a residual) and rstd;
+    workspace is a uint8 tensor of dsa_rmsnorm_backward_workspace_size bytes."""
+    w = "dsa_rmsnorm_backward"
+    dtype = _on_device(w, dy, 2)
+    rows, cols = shape = tuple(dy.shape)
+    gp, gl = _strided(w, "dy", dy, dy.dtype, shape)
+    hp, hl = _strided(w, "h", h, dy.dtype, shape)
+    rp, rl = _strided(w, "dresidual", dresidual, dy.dtype, shape)
+    op, ol = _strided(w, "dh", dh, dy.dtype, shape)
+    size = workspace.numel() * workspace.element_size()
+    _check(_lib.dsa_rmsnorm_backward(gp, gl, hp, hl, _dense(w, "weight", weight, dy.dtype, (cols,)),
+                                     _dense(w, "rstd", rstd, torch.float32, (rows,)), rp, rl, rows, cols, dtype, op, ol,
+                                     _dense(w, "dw", dw, torch.float32, (cols,)),
+                                     _dense(w, "workspace", workspace, workspace.dtype, workspace.shape), size,
+                                     _stream(stream)), w)
+    return dh, dw
+
+
+def dsa_rope(x, positions, freqs, out, rot_offset, rot_dim, layout=DSA_ROPE_INTERLEAVED, mscale=1.0, transpose=False,
+             stream=None):
+    """Rotates dims [rot_offset, rot_offset + rot_dim) of every head of x [rows, heads, dim] by
+    positions[row] * freqs (int32 [rows], float64 [rot_dim / 2]) into out, which is x itself or of
+    its shape (the other dims are then copied).  transpose gives the backward pass."""
+    w = "dsa_rope"
+    dtype = _on_device(w, x, 3)
+    rows, heads, dim = shape = tuple(x.shape)
+    xp, xl = _strided(w, "x", x, x.dtype, shape)
+    op, ol = _strided(w, "out", out, x.dtype, shape)
+    _check(_lib.dsa_rope(xp, xl, x.stride(1), op, ol, out.stride(1), rows, heads, dim, int(rot_offset), int(rot_dim),
+                         int(layout), dtype, _dense(w, "positions", positions, torch.int32, (rows,)),
+                         _dense(w, "freqs", freqs, torch.float64, (int(rot_dim) // 2,)), float(mscale), int(bool(transpose)),
+                         _stream(stream)), w)
+    return out
+
+
+def dsa_rope_frequencies(rot_dim, theta, scaling=DSA_ROPE_PLAIN, factor=1.0, original_ctx=0.0, beta_fast=32.0, beta_slow=1.0):
+    """(freqs, mscale): the float64 CPU tensor [rot_dim / 2] of radians per position, plain or scaled
+    for a context `factor` times original_ctx, and the factor on the rotated values (host only)."""
+    freqs = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float64)
+    mscale = _F32(1.0)
+    _check(_lib.dsa_rope_frequencies(int(rot_dim), float(theta), int(scaling), float(factor), float(original_ctx),
+                                     float(beta_fast), float(beta_slow), freqs.data_ptr(), ctypes.byref(mscale)),
+           "dsa_rope_frequencies")
+    return freqs, float(mscale.value)
+
+
+def dsa_cache_append(kv, kv_weight, eps, key, seq, positions, freqs, latent: Desc, keys: Desc, layout=DSA_ROPE_INTERLEAVED,
+                     key_layout=DSA_ROPE_HALF, key_rot_offset=0, mscale=1.0, stream=None):
+    """Writes row r's latent (kv[r] bf16 [576]: 512 dims RMS-normalised with kv_weight, 64 rotated) and
+    indexer key (key[r] bf16 [d_I]: 64 dims from key_rot_offset rotated, then e4m3 with a scale) to
+    position positions[r] of sequence seq[r] (seq None: sequence r; -1: skipped) of the caches that
+    latent and keys describe.  kv, kv_weight and latent, or key and keys, may be None."""
+    w = "dsa_cache_append"
+    if positions.get_device() < 0:
+        raise ValueError(f"{w}: tensors must be on a CUDA device, got {positions.device}")
+    rows = positions.shape[0]
+    kp, kl, d_I = None, 0, 128
+    vp, vl = _strided(w, "kv", kv, torch.bfloat16, (rows, 576))
+    if key is not None:
+        d_I = key.shape[-1]
+        kp, kl = _strided(w, "key", key, torch.bfloat16, (rows, d_I))
+    for name, desc, kind, width in (("latent", latent, torch.bfloat16, 576), ("keys", keys, torch.uint8, d_I)):
+        if desc is not None and (desc._refs[0].dtype is not kind or desc._refs[0].shape[-1] != width
+                                 or not desc._refs[0].is_contiguous()):
+            raise ValueError(f"{w}: {name} must describe a contiguous {kind} cache with rows of {width}")
+    if latent is not None and keys is not None and latent.batch != keys.batch:
+        raise ValueError(f"{w}: latent describes {latent.batch} sequences, keys {keys.batch}")
+    batch = latent.batch if latent is not None else keys.batch if keys is not None else 0
+    _check(_lib.dsa_cache_append(vp, vl, _dense(w, "kv_weight", kv_weight, torch.bfloat16, (512,)), float(eps), kp, kl, d_I,
+                                 _dense(w, "seq", seq, torch.int32, (rows,)),
+                                 _dense(w, "positions", positions, torch.int32, (rows,)), rows, batch,
+                                 _dense(w, "freqs", freqs, torch.float64, (32,)), float(mscale), int(layout),
+                                 int(key_layout), int(key_rot_offset), None if latent is None else latent.ref(),
+                                 None if keys is None else keys.ref(), _stream(stream)), w)
+
+
+def _window_args(w, q, latent, B, H, out, lse):
+    rows = q.shape[0]
+    if q.get_device() < 0:
+        raise ValueError(f"{w}: tensors must be on a CUDA device, got {q.device}")
+    if latent._refs[0].dtype is not torch.bfloat16 or latent._refs[0].shape[-1] != 576 or not latent._refs[0].is_contiguous():
+        raise ValueError(f"{w}: latent must describe contiguous bf16 rows of 576")
+    if latent.batch != B:
+        raise ValueError(f"{w}: latent describes {latent.batch} sequences, B = {B}")
+    return (_dense(w, "q", q, torch.bfloat16, (rows, H, 576)), _dense(w, "out", out, torch.bfloat16, (rows, H, 512)),
+            _dense(w, "lse", lse, torch.float32, (rows, H)))
+
+
+def dsa_window_mla_prefill(q, latent: Desc, B, H, window, sinks, sm_scale, out, lse=None, stream=None):
+    """MLA attention of packed prefill tokens over their last `window` keys and the first `sinks`
+    tokens of their sequence (dense causal attention when window covers the sequence)."""
+    w = "dsa_window_mla_prefill"
+    qp, op, lp = _window_args(w, q, latent, int(B), int(H), out, lse)
+    if latent.struct.kind == DSA_KV_CONTIGUOUS and q.shape[0] != latent.struct.total_tokens:
+        raise ValueError(f"{w}: q has {q.shape[0]} rows, latent {latent.struct.total_tokens} tokens")
+    _check(_lib.dsa_window_mla_prefill(qp, latent.ref(), int(B), int(H), int(window), int(sinks), float(sm_scale), op, lp,
+                                       _stream(stream)), w)
+    return out
+
+
+def dsa_window_mla_workspace_size(B, H, window, sinks, max_ctx) -> int:
+    return int(_lib.dsa_window_mla_workspace_size(int(B), int(H), int(window), int(sinks), int(max_ctx)))
+
+
+def dsa_window_mla_decode(q, latent: Desc, B, H, window, sinks, sm_scale, out, lse=None, workspace=None, stream=None):
+    """The same for one query per sequence at position ctx - 1 over the paged latent cache;
+    workspace: dsa_window_mla_workspace_size bytes (None where that is 0)."""
+    w = "dsa_window_mla_decode"
+    qp, op, lp = _window_args(w, q, latent, int(B), int(H), out, lse)
+    if q.shape[0] != B:
+        raise ValueError(f"{w}: q has {q.shape[0]} rows, B = {B}")
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    wp = None if workspace is None else _dense(w, "workspace", workspace, workspace.dtype, workspace.shape)
+    _check(_lib.dsa_window_mla_decode(qp, latent.ref(), int(B), int(H), int(window), int(sinks), float(sm_scale), op, lp, wp,
+                                      size, _stream(stream)), w)
+    return out

@@ -5,12 +5,16 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/dsa.h"
 #include "common.cuh"
+#include "cache_append.cuh"
 #include "indexer.cuh"
 #include "quantize.cuh"
 #include "attn_probs.cuh"
@@ -18,6 +22,8 @@
 #include "indexer_kl.cuh"
 #include "selftest.cuh"
 #include "mla_common.cuh"
+#include "rmsnorm.cuh"
+#include "rope.cuh"
 #include "sparse_mla_pair.cuh"
 #include "topk.cuh"
 
@@ -217,16 +223,16 @@ int decode_splits(int B, int k) {
   return s;
 }
 
-// Sparse prefill, masked prefill and decode: the head-split pair kernel.  Q is read by TMA as a
+// Sparse, masked and window prefill, and decode: the head-split pair kernel.  Q is read by TMA as a
 // [q_rows * H, 576] bf16 matrix in 64 x 64 tiles (128-byte swizzle).
-template <bool DECODE, bool MASKED = false>
+template <bool DECODE, int FORM = kMlaSparse>
 dsa_status launch_mla_pair(const void* latent, const void* q, int64_t q_rows, const MlaParams& p, int64_t units,
                            cudaStream_t s) {
   CUtensorMap qm;
   if (!make_map_2d(&qm, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kLatentDim, static_cast<uint64_t>(q_rows) * p.H,
                    kLatentDim * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
     return DSA_ERR_INVALID_ARGUMENT;
-  auto kern = sparse_mla_pair_kernel<DECODE, MASKED>;
+  auto kern = sparse_mla_pair_kernel<DECODE, FORM>;
   const int smem = mlap::kSmemBytes + 1024;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return DSA_ERR_CUDA;
@@ -235,7 +241,168 @@ dsa_status launch_mla_pair(const void* latent, const void* q, int64_t q_rows, co
   return launch_status();
 }
 
+// Window decode: splits per sequence.  A unit (sequence, split) costs its 64-key chunks plus about
+// kUnitChunks chunks' time for its Q load, pipeline fill and O readout, and the units run in
+// rounds over the CTA pairs; the split count with the least rounds x (chunks + kUnitChunks) is
+// taken, the smaller of equals (fewer partial results).  Unlike the selection's decode_splits it
+// need not divide anything: the kernel deals a sequence's chunks out evenly.
+constexpr int kUnitChunks = 6;
+
+int window_splits(int B, int window, int sinks, int max_ctx) {
+  const int64_t keys = std::min<int64_t>(max_ctx, static_cast<int64_t>(window) + sinks);
+  const int64_t chunks = (keys + 63) / 64;
+  int64_t best = 0;
+  int splits = 1;
+  for (int s = 1; s <= kMlaClusters && s <= std::max<int64_t>(chunks, 1); ++s) {
+    const int64_t rounds = (static_cast<int64_t>(B) * s + kMlaClusters - 1) / kMlaClusters;
+    const int64_t cost = rounds * ((chunks + s - 1) / s + kUnitChunks);
+    if (s == 1 || cost < best) {
+      best = cost;
+      splits = s;
+    }
+  }
+  return splits;
+}
+
 bool mla_shape_ok(int H, int k) { return H >= 1 && H <= 128 && k >= 64 && k <= 2048 && k % 64 == 0; }
+
+// ---- row operators: norm, rotary positions, cache append ---------------------------------------
+constexpr int kSms = 148;
+
+bool dtype_ok(int32_t dtype) { return dtype == DSA_BF16 || dtype == DSA_F16 || dtype == DSA_F32; }
+size_t dtype_size(int32_t dtype) { return dtype == DSA_F32 ? 4 : 2; }
+
+// Calls f with a null pointer of the element type of `dtype`.
+template <typename F>
+dsa_status with_dtype(int32_t dtype, F f) {
+  if (dtype == DSA_BF16) return f(static_cast<__nv_bfloat16*>(nullptr));
+  if (dtype == DSA_F16) return f(static_cast<__half*>(nullptr));
+  return f(static_cast<float*>(nullptr));
+}
+
+// Whether a [rows, cols] operand (null: absent) can be read in aligned pieces of 8 elements.
+bool wide(const void* p, int64_t ld) { return p == nullptr || (aligned(p, 16) && ld % 8 == 0); }
+
+// Pieces of 8 elements per thread and threads per row for a CTA-wide row: at least 2 pieces per
+// thread (two 16-byte loads in flight each) where that leaves at most max_threads.
+void row_shape(int cols, int max_threads, int min_pieces, int* pieces, int* threads) {
+  const int n = cols / 8;
+  int ch = min_pieces;
+  while (ch < 4 && (n + ch - 1) / ch > max_threads) ch *= 2;
+  *pieces = ch;
+  *threads = ((n + ch - 1) / ch + 31) / 32 * 32;
+}
+
+template <typename T>
+dsa_status launch_rmsnorm(const NormParams& p, bool vector, cudaStream_t s) {
+  const unsigned rows = static_cast<unsigned>(p.rows);
+  if (!vector || p.cols > 4 * 8 * 1024) {
+    rmsnorm_general_kernel<T><<<rows, norm::kGeneralThreads, 0, s>>>(p);
+    return launch_status();
+  }
+  if (p.cols <= norm::kWarpCols) {
+    const unsigned grid = (rows + norm::kWarpRows - 1) / norm::kWarpRows;
+    const int ch = (p.cols + 255) / 256;
+    if (ch <= 1) rmsnorm_kernel<T, 1, true><<<grid, norm::kWarpRows * 32, 0, s>>>(p);
+    else if (ch <= 2) rmsnorm_kernel<T, 2, true><<<grid, norm::kWarpRows * 32, 0, s>>>(p);
+    else rmsnorm_kernel<T, 4, true><<<grid, norm::kWarpRows * 32, 0, s>>>(p);
+    return launch_status();
+  }
+  int ch, threads;
+  row_shape(p.cols, 1024, p.rows <= kSms ? 1 : 2, &ch, &threads);
+  if (ch == 1) rmsnorm_kernel<T, 1, false><<<rows, threads, 0, s>>>(p);
+  else if (ch == 2) rmsnorm_kernel<T, 2, false><<<rows, threads, 0, s>>>(p);
+  else rmsnorm_kernel<T, 4, false><<<rows, threads, 0, s>>>(p);
+  return launch_status();
+}
+
+// CTAs of the backward (each writes one row of partial sums of dw).
+constexpr int kNormBwdCtas = 4 * kSms;
+int64_t norm_bwd_ctas(int64_t rows) { return rows < kNormBwdCtas ? rows : kNormBwdCtas; }
+
+template <typename T>
+dsa_status launch_rmsnorm_backward(const NormBwdParams& p, bool vector, float* dw, cudaStream_t s) {
+  const int64_t most = norm_bwd_ctas(p.rows);
+  unsigned grid;
+  if (!vector || p.cols > 4 * 8 * 512) {
+    grid = static_cast<unsigned>(most);
+    rmsnorm_backward_general_kernel<T><<<grid, norm::kGeneralThreads, 0, s>>>(p);
+  } else if (p.cols <= norm::kWarpCols) {
+    grid = static_cast<unsigned>(std::min<int64_t>(most, (p.rows + norm::kWarpRows - 1) / norm::kWarpRows));
+    const int ch = (p.cols + 255) / 256;
+    if (ch <= 1) rmsnorm_backward_kernel<T, 1, true><<<grid, norm::kWarpRows * 32, 0, s>>>(p);
+    else if (ch <= 2) rmsnorm_backward_kernel<T, 2, true><<<grid, norm::kWarpRows * 32, 0, s>>>(p);
+    else rmsnorm_backward_kernel<T, 4, true><<<grid, norm::kWarpRows * 32, 0, s>>>(p);
+  } else {
+    grid = static_cast<unsigned>(most);
+    int ch, threads;
+    row_shape(p.cols, 512, 1, &ch, &threads);
+    if (ch == 1) rmsnorm_backward_kernel<T, 1, false><<<grid, threads, 0, s>>>(p);
+    else if (ch == 2) rmsnorm_backward_kernel<T, 2, false><<<grid, threads, 0, s>>>(p);
+    else rmsnorm_backward_kernel<T, 4, false><<<grid, threads, 0, s>>>(p);
+  }
+  const dsa_status st = launch_status();
+  if (st != DSA_OK) return st;
+  rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 256, 0, s>>>(p.part, static_cast<int>(grid), p.cols, dw);
+  return launch_status();
+}
+
+template <typename T>
+dsa_status launch_rope(RopeParams p, bool vector, cudaStream_t s) {
+  const int pairs = p.rot / 2;
+  const int rest = p.copy_rest ? p.dim - p.rot : 0;
+  if (vector) p.items_per_head = p.rot / (p.half_layout ? 16 : 8) + rest / 8;
+  else p.items_per_head = pairs + rest;
+  // A CTA moves about kUnroll items per thread: several rows when a row has fewer, a range of a
+  // row's heads when it has more (each range forms its own table: rot / 2 entries).
+  const int64_t target = rope::kThreads * (vector ? rope::kUnroll : 8);
+  const int64_t per_row = static_cast<int64_t>(p.heads) * p.items_per_head;
+  int64_t parts = 1;
+  p.rows_per_cta = 1;
+  p.heads_per_cta = p.heads;
+  if (per_row >= 2 * target) {
+    p.heads_per_cta = static_cast<int32_t>(std::max<int64_t>(1, target / p.items_per_head));
+    parts = (p.heads + p.heads_per_cta - 1) / p.heads_per_cta;
+    if (parts > 65535) {
+      parts = 65535;
+      p.heads_per_cta = static_cast<int32_t>((p.heads + parts - 1) / parts);
+      parts = (p.heads + p.heads_per_cta - 1) / p.heads_per_cta;
+    }
+  } else {
+    int64_t r = std::min<int64_t>(target / per_row, rope::kTable / pairs);
+    // few rows: spread them over the GPU first
+    r = std::min<int64_t>(r, (p.rows + kSms - 1) / kSms);
+    p.rows_per_cta = static_cast<int32_t>(std::max<int64_t>(1, r));
+  }
+  const int64_t ctas = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
+  const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(parts));
+  if (!vector) rope_general_kernel<T><<<grid, rope::kThreads, 0, s>>>(p);
+  else if (p.half_layout) rope_kernel<T, true><<<grid, rope::kThreads, 0, s>>>(p);
+  else rope_kernel<T, false><<<grid, rope::kThreads, 0, s>>>(p);
+  return launch_status();
+}
+
+// One cache of dsa_cache_append from its descriptor.
+dsa_status append_cache(const dsa_kv_desc* d, bool with_scale, size_t align, AppendCache* c) {
+  if (d->data == nullptr || !aligned(d->data, align) || (with_scale && d->scale == nullptr) || d->max_seqlen <= 0)
+    return DSA_ERR_INVALID_ARGUMENT;
+  c->data = const_cast<void*>(d->data);
+  c->scale = const_cast<float*>(d->scale);
+  c->max_seqlen = d->max_seqlen;
+  if (d->kind == DSA_KV_CONTIGUOUS) {
+    if (d->cu_seqlens == nullptr || d->total_tokens <= 0) return DSA_ERR_INVALID_ARGUMENT;
+    c->cu = d->cu_seqlens;
+    c->rows = d->total_tokens;
+    return DSA_OK;
+  }
+  if (d->kind != DSA_KV_PAGED || d->block_table == nullptr || d->num_blocks <= 0 || d->max_blocks_per_seq <= 0)
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (d->block_size != 64) return DSA_ERR_UNSUPPORTED;
+  c->table = d->block_table;
+  c->rows = d->num_blocks;
+  c->max_blocks = d->max_blocks_per_seq;
+  return DSA_OK;
+}
 
 // ---- decode with library-held scratch (no allocation on the call path) ---------------------
 // One array per device, in this translation unit.  Host code cannot pass the symbol itself to
@@ -642,7 +809,7 @@ dsa_status dsa_masked_mla_prefill(const void* q, const dsa_kv_desc* latent, cons
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
-  return launch_mla_pair<false, true>(latent->data, q, p.rows, p, p.rows, as_stream(stream));
+  return launch_mla_pair<false, kMlaMasked>(latent->data, q, p.rows, p, p.rows, as_stream(stream));
 }
 
 dsa_status dsa_sparse_mla_decode(const void* q, const dsa_kv_desc* latent, const int32_t* idx, int32_t B, int32_t H,
@@ -684,7 +851,7 @@ dsa_status dsa_sparse_mla_decode(const void* q, const dsa_kv_desc* latent, const
   dsa_status st = launch_mla_pair<true>(latent->data, q, B, p, static_cast<int64_t>(B) * splits, s);
   if (st != DSA_OK) return st;
   if (splits == 1) return DSA_OK;
-  mla_combine_kernel<<<dim3(H, B), 128, 0, s>>>(p.part_o, p.part_ml, splits, H, static_cast<__nv_bfloat16*>(out), lse);
+  mla_combine_kernel<false><<<dim3(H, B), 128, 0, s>>>(p.part_o, p.part_ml, splits, H, static_cast<__nv_bfloat16*>(out), lse);
   return launch_status();
 }
 
@@ -772,6 +939,303 @@ size_t dsa_workspace_size(int32_t mode, int32_t B, int64_t total_tokens, int32_t
   if (mode == DSA_MODE_PREFILL) return align256(static_cast<size_t>(total_tokens > 0 ? total_tokens : 0) * k * 4);
   return decode_partials_bytes(B, H, decode_splits(B, k)) + dsa_decode_select_workspace_size(B, max_ctx) +
          align256(static_cast<size_t>(B) * k * 4);
+}
+
+dsa_status dsa_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual, const void* weight,
+                       int64_t rows, int32_t cols, int32_t dtype, float eps, void* y, int64_t ld_y,
+                       void* residual_out, int64_t ld_residual_out, uint8_t* codes, float* scale, int32_t group,
+                       float* rstd, void* stream) {
+  if (rows < 0 || !dtype_ok(dtype) || cols <= 0 || !(eps >= 0.f) || !std::isfinite(eps)) return DSA_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return DSA_OK;
+  if (x == nullptr || weight == nullptr || (y == nullptr && codes == nullptr) || (codes == nullptr) != (scale == nullptr))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (group != 0 && group != DSA_QUANT_GROUP) return DSA_ERR_INVALID_ARGUMENT;
+  const size_t es = dtype_size(dtype);
+  if (!aligned(x, es) || !aligned(residual, es) || !aligned(weight, es) || !aligned(y, es) || !aligned(residual_out, es) ||
+      !aligned(scale, 4) || !aligned(rstd, 4))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (ld_x < cols || (residual != nullptr && ld_residual < cols) || (y != nullptr && ld_y < cols) ||
+      (residual_out != nullptr && ld_residual_out < cols))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
+  NormParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = x;
+  p.res = residual;
+  p.w = weight;
+  p.ld_x = ld_x;
+  p.ld_res = ld_residual;
+  p.ld_y = ld_y;
+  p.ld_ro = ld_residual_out;
+  p.rows = rows;
+  p.cols = cols;
+  p.eps = eps;
+  p.y = y;
+  p.res_out = residual_out;
+  p.codes = codes;
+  p.scale = scale;
+  p.groups = group == 0 ? 0 : cols / DSA_QUANT_GROUP + (cols % DSA_QUANT_GROUP != 0);
+  p.rstd = rstd;
+  const bool vector = cols % 8 == 0 && wide(x, ld_x) && wide(residual, ld_residual) && wide(weight, 0) && wide(y, ld_y) &&
+                      wide(residual_out, ld_residual_out) && aligned(codes, 8);
+  return with_dtype(dtype, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return launch_rmsnorm<T>(p, vector, as_stream(stream));
+  });
+}
+
+size_t dsa_rmsnorm_backward_workspace_size(int64_t rows, int32_t cols) {
+  if (rows <= 0 || cols <= 0) return 0;
+  return align256(static_cast<size_t>(norm_bwd_ctas(rows)) * cols * sizeof(float));
+}
+
+dsa_status dsa_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* weight,
+                                const float* rstd, const void* dresidual, int64_t ld_dresidual, int64_t rows,
+                                int32_t cols, int32_t dtype, void* dh, int64_t ld_dh, float* dw, void* workspace,
+                                size_t ws_bytes, void* stream) {
+  if (rows < 0 || !dtype_ok(dtype) || cols <= 0 || dw == nullptr || !aligned(dw, 4)) return DSA_ERR_INVALID_ARGUMENT;
+  cudaStream_t s = as_stream(stream);
+  if (rows == 0)
+    return cudaMemsetAsync(dw, 0, static_cast<size_t>(cols) * sizeof(float), s) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  if (dy == nullptr || h == nullptr || weight == nullptr || rstd == nullptr || dh == nullptr || workspace == nullptr)
+    return DSA_ERR_INVALID_ARGUMENT;
+  const size_t es = dtype_size(dtype);
+  if (!aligned(dy, es) || !aligned(h, es) || !aligned(weight, es) || !aligned(dresidual, es) || !aligned(dh, es) ||
+      !aligned(rstd, 4) || !aligned(workspace, 16))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (ld_dy < cols || ld_h < cols || ld_dh < cols || (dresidual != nullptr && ld_dresidual < cols))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
+  if (ws_bytes < dsa_rmsnorm_backward_workspace_size(rows, cols)) return DSA_ERR_WORKSPACE_TOO_SMALL;
+  NormBwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.dy = dy;
+  p.h = h;
+  p.w = weight;
+  p.rstd = rstd;
+  p.dres = dresidual;
+  p.ld_dy = ld_dy;
+  p.ld_h = ld_h;
+  p.ld_dres = ld_dresidual;
+  p.ld_dh = ld_dh;
+  p.rows = rows;
+  p.cols = cols;
+  p.dh = dh;
+  p.part = static_cast<float*>(workspace);
+  const bool vector = cols % 8 == 0 && wide(dy, ld_dy) && wide(h, ld_h) && wide(weight, 0) && wide(dresidual, ld_dresidual) &&
+                      wide(dh, ld_dh);
+  return with_dtype(dtype, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return launch_rmsnorm_backward<T>(p, vector, dw, s);
+  });
+}
+
+dsa_status dsa_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride, void* out, int64_t out_row_stride,
+                    int64_t out_head_stride, int64_t rows, int32_t heads, int32_t dim, int32_t rot_offset,
+                    int32_t rot_dim, int32_t layout, int32_t dtype, const int32_t* positions, const double* freqs,
+                    float mscale, int32_t transpose, void* stream) {
+  if (rows < 0 || heads < 0 || dim <= 0 || !dtype_ok(dtype) || !std::isfinite(mscale)) return DSA_ERR_INVALID_ARGUMENT;
+  if (layout != DSA_ROPE_INTERLEAVED && layout != DSA_ROPE_HALF) return DSA_ERR_INVALID_ARGUMENT;
+  if (rot_dim < 2 || rot_dim % 2 != 0 || rot_offset < 0 || rot_dim > dim || rot_offset > dim - rot_dim)
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (rows == 0 || heads == 0) return DSA_OK;
+  if (x == nullptr || out == nullptr || positions == nullptr || freqs == nullptr) return DSA_ERR_INVALID_ARGUMENT;
+  const size_t es = dtype_size(dtype);
+  if (!aligned(x, es) || !aligned(out, es) || !aligned(positions, 4) || !aligned(freqs, 8)) return DSA_ERR_INVALID_ARGUMENT;
+  if ((heads > 1 && (x_head_stride < dim || out_head_stride < dim)) || (rows > 1 && (x_row_stride < dim || out_row_stride < dim)))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (out == x && ((rows > 1 && x_row_stride != out_row_stride) || (heads > 1 && x_head_stride != out_head_stride)))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (rot_dim > 2 * rope::kMaxPairs || rows > 0x7FFFFFFFLL || static_cast<int64_t>(heads) * dim > 0x7FFFFFFFLL)
+    return DSA_ERR_UNSUPPORTED;
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = x;
+  p.out = out;
+  p.xr = x_row_stride;
+  p.xh = x_head_stride;
+  p.orow = out_row_stride;
+  p.oh = out_head_stride;
+  p.rows = rows;
+  p.heads = heads;
+  p.dim = dim;
+  p.rot0 = rot_offset;
+  p.rot = rot_dim;
+  p.half_layout = layout == DSA_ROPE_HALF;
+  p.pos = positions;
+  p.freqs = freqs;
+  p.mscale = mscale;
+  p.transpose = transpose;
+  p.copy_rest = out != x;
+  const int piece = layout == DSA_ROPE_HALF ? 16 : 8;  // both halves of a pair lie in whole pieces
+  auto strides_ok = [](int64_t row, int64_t head, int64_t r, int h) { return (r <= 1 || row % 8 == 0) && (h <= 1 || head % 8 == 0); };
+  const bool vector = dim % 8 == 0 && rot_offset % 8 == 0 && rot_dim % piece == 0 && aligned(x, 16) && aligned(out, 16) &&
+                      strides_ok(x_row_stride, x_head_stride, rows, heads) &&
+                      strides_ok(out_row_stride, out_head_stride, rows, heads);
+  return with_dtype(dtype, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return launch_rope<T>(p, vector, as_stream(stream));
+  });
+}
+
+dsa_status dsa_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling, double factor, double original_ctx,
+                                double beta_fast, double beta_slow, double* freqs, float* mscale) {
+  if (freqs == nullptr || mscale == nullptr || rot_dim < 2 || rot_dim % 2 != 0 || !(theta > 1.0) || !std::isfinite(theta))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (scaling < DSA_ROPE_PLAIN || scaling > DSA_ROPE_YARN) return DSA_ERR_INVALID_ARGUMENT;
+  if (scaling != DSA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return DSA_ERR_INVALID_ARGUMENT;
+  if (scaling == DSA_ROPE_NTK && rot_dim < 4) return DSA_ERR_INVALID_ARGUMENT;
+  double low = 0.0, span = 1.0;
+  if (scaling == DSA_ROPE_YARN) {
+    if (!(original_ctx > 0.0) || !std::isfinite(original_ctx) || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) ||
+        !std::isfinite(beta_fast))
+      return DSA_ERR_INVALID_ARGUMENT;
+    const double two_pi = 6.283185307179586;
+    auto dim_of = [&](double turns) { return rot_dim * std::log(original_ctx / (two_pi * turns)) / (2.0 * std::log(theta)); };
+    low = std::max(std::floor(dim_of(beta_fast)), 0.0);
+    const double high = std::min(std::ceil(dim_of(beta_slow)), rot_dim - 1.0);
+    span = std::max(high - low, 0.001);
+  }
+  const double base = scaling == DSA_ROPE_NTK ? theta * std::pow(factor, rot_dim / (rot_dim - 2.0)) : theta;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / rot_dim);
+    if (scaling == DSA_ROPE_LINEAR) {
+      freqs[i] = f / factor;
+    } else if (scaling == DSA_ROPE_YARN) {
+      const double ramp = std::min(std::max((i - low) / span, 0.0), 1.0);
+      freqs[i] = f / factor * ramp + f * (1.0 - ramp);
+    } else {
+      freqs[i] = f;
+    }
+  }
+  *mscale = scaling == DSA_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return DSA_OK;
+}
+
+dsa_status dsa_cache_append(const void* kv, int64_t ld_kv, const void* kv_weight, float eps, const void* key,
+                            int64_t ld_key, int32_t d_I, const int32_t* seq, const int32_t* positions, int64_t rows,
+                            int32_t B, const double* freqs, float mscale, int32_t layout, int32_t key_layout,
+                            int32_t key_rot_offset, const dsa_kv_desc* latent, const dsa_kv_desc* keys, void* stream) {
+  if (rows < 0 || B <= 0 || !std::isfinite(mscale)) return DSA_ERR_INVALID_ARGUMENT;
+  if ((kv == nullptr) != (latent == nullptr) || (key == nullptr) != (keys == nullptr) || (kv == nullptr && key == nullptr))
+    return rows == 0 ? DSA_OK : DSA_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return DSA_OK;
+  if (positions == nullptr || freqs == nullptr || !aligned(freqs, 8)) return DSA_ERR_INVALID_ARGUMENT;
+  AppendParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (latent != nullptr) {
+    if (kv_weight == nullptr || !aligned(kv, 16) || !aligned(kv_weight, 16) || ld_kv % 8 != 0 || (rows > 1 && ld_kv < kLatentDim))
+      return DSA_ERR_INVALID_ARGUMENT;
+    if (!(eps >= 0.f) || !std::isfinite(eps) || (layout != DSA_ROPE_INTERLEAVED && layout != DSA_ROPE_HALF))
+      return DSA_ERR_INVALID_ARGUMENT;
+    const dsa_status st = append_cache(latent, false, 16, &p.latent);
+    if (st != DSA_OK) return st;
+  }
+  if (keys != nullptr) {
+    if (d_I != 64 && d_I != 128) return DSA_ERR_UNSUPPORTED;
+    if (!aligned(key, 4) || ld_key % 2 != 0 || (rows > 1 && ld_key < d_I)) return DSA_ERR_INVALID_ARGUMENT;
+    if (key_layout != DSA_ROPE_INTERLEAVED && key_layout != DSA_ROPE_HALF) return DSA_ERR_INVALID_ARGUMENT;
+    if (key_rot_offset < 0 || key_rot_offset > d_I - 64 || key_rot_offset % 2 != 0) return DSA_ERR_INVALID_ARGUMENT;
+    const dsa_status st = append_cache(keys, true, 2, &p.keys);
+    if (st != DSA_OK) return st;
+  }
+  if (rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
+  p.kv = static_cast<const __nv_bfloat16*>(kv);
+  p.w = static_cast<const __nv_bfloat16*>(kv_weight);
+  p.key = static_cast<const __nv_bfloat16*>(key);
+  p.ld_kv = ld_kv;
+  p.ld_key = ld_key;
+  p.eps = eps;
+  p.seq = seq;
+  p.pos = positions;
+  p.rows = rows;
+  p.B = B;
+  p.freqs = freqs;
+  p.mscale = mscale;
+  p.half = layout == DSA_ROPE_HALF;
+  p.key_half = key_layout == DSA_ROPE_HALF;
+  p.key_rot0 = key_rot_offset;
+  const unsigned grid = static_cast<unsigned>((rows + append::kWarps - 1) / append::kWarps);
+  if (keys != nullptr && d_I == 64) cache_append_kernel<64><<<grid, append::kWarps * 32, 0, as_stream(stream)>>>(p);
+  else cache_append_kernel<128><<<grid, append::kWarps * 32, 0, as_stream(stream)>>>(p);
+  return launch_status();
+}
+
+// Arguments common to both window entries; fills what they share.
+static dsa_status window_common(const void* q, const dsa_kv_desc* latent, int32_t B, int32_t H, int32_t window,
+                                int32_t sinks, float sm_scale, void* out, float* lse, MlaParams* p) {
+  if (q == nullptr || latent == nullptr || latent->data == nullptr || out == nullptr || B <= 0)
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(latent->data, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSA_ERR_INVALID_ARGUMENT;
+  if (window < 1 || sinks < 0 || !(sm_scale >= 0.f) || !std::isfinite(sm_scale) || latent->max_seqlen <= 0)
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (H < 1 || H > 128) return DSA_ERR_UNSUPPORTED;
+  std::memset(p, 0, sizeof(*p));
+  p->q = static_cast<const __nv_bfloat16*>(q);
+  p->B = B;
+  p->H = H;
+  p->splits = 1;
+  p->window = window;
+  p->sinks = sinks;
+  p->scale_log2 = sm_scale * 1.4426950408889634f;
+  p->out = static_cast<__nv_bfloat16*>(out);
+  p->lse = lse;
+  return DSA_OK;
+}
+
+dsa_status dsa_window_mla_prefill(const void* q, const dsa_kv_desc* latent, int32_t B, int32_t H, int32_t window,
+                                  int32_t sinks, float sm_scale, void* out, float* lse, void* stream) {
+  MlaParams p;
+  const dsa_status st = window_common(q, latent, B, H, window, sinks, sm_scale, out, lse, &p);
+  if (st != DSA_OK) return st;
+  if (latent->kind != DSA_KV_CONTIGUOUS || latent->cu_seqlens == nullptr || latent->total_tokens <= 0)
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (latent->total_tokens * H > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
+  p.cu_seqlens = latent->cu_seqlens;
+  p.rows = latent->total_tokens;
+  return launch_mla_pair<false, kMlaWindow>(latent->data, q, p.rows, p, p.rows, as_stream(stream));
+}
+
+size_t dsa_window_mla_workspace_size(int32_t B, int32_t H, int32_t window, int32_t sinks, int32_t max_ctx) {
+  if (B <= 0 || H <= 0 || window < 1 || sinks < 0 || max_ctx <= 0) return 0;
+  const int splits = window_splits(B, window, sinks, max_ctx);
+  return splits == 1 ? 0 : decode_partials_bytes(B, H, splits);
+}
+
+dsa_status dsa_window_mla_decode(const void* q, const dsa_kv_desc* latent, int32_t B, int32_t H, int32_t window,
+                                 int32_t sinks, float sm_scale, void* out, float* lse, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+  MlaParams p;
+  dsa_status st = window_common(q, latent, B, H, window, sinks, sm_scale, out, lse, &p);
+  if (st != DSA_OK) return st;
+  if (latent->kind != DSA_KV_PAGED || latent->block_table == nullptr || latent->context_lens == nullptr ||
+      latent->num_blocks <= 0 || latent->max_blocks_per_seq <= 0)
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (latent->block_size != 64) return DSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(latent->max_seqlen) > static_cast<int64_t>(latent->max_blocks_per_seq) * 64)
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (static_cast<int64_t>(latent->num_blocks) * 64 > 0x7FFFFFFFLL || static_cast<int64_t>(B) * H > 0x7FFFFFFFLL)
+    return DSA_ERR_UNSUPPORTED;
+  p.splits = window_splits(B, window, sinks, latent->max_seqlen);
+  if (p.splits > 1) {
+    if (workspace == nullptr || !aligned(workspace, 256)) return DSA_ERR_INVALID_ARGUMENT;
+    if (ws_bytes < decode_partials_bytes(B, H, p.splits)) return DSA_ERR_WORKSPACE_TOO_SMALL;
+    if (B > 65535) return DSA_ERR_UNSUPPORTED;  // the merge's grid
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                         align256(static_cast<size_t>(B) * p.splits * H * kValueDim * 4));
+  }
+  p.block_table = latent->block_table;
+  p.context_lens = latent->context_lens;
+  p.max_blocks_per_seq = latent->max_blocks_per_seq;
+  p.num_blocks = latent->num_blocks;
+  p.max_len = latent->max_seqlen;
+  p.rows = B;
+  cudaStream_t s = as_stream(stream);
+  st = launch_mla_pair<true, kMlaWindow>(latent->data, q, B, p, static_cast<int64_t>(B) * p.splits, s);
+  if (st != DSA_OK || p.splits == 1) return st;
+  mla_combine_kernel<true><<<dim3(H, B), 128, 0, s>>>(p.part_o, p.part_ml, p.splits, H, p.out, lse);
+  return launch_status();
 }
 
 }  // extern "C"

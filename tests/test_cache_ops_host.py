@@ -1,0 +1,197 @@
+"""Host side of the operators around the caches: every refusal that needs no GPU (the calls return
+before a launch), the frequency tables, the workspace rules."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import sparse_attention_09_b200 as dsa
+
+INVALID, UNSUPPORTED, SMALL, OK = dsa.DSA_ERR_INVALID_ARGUMENT, dsa.DSA_ERR_UNSUPPORTED, dsa.DSA_ERR_WORKSPACE_TOO_SMALL, dsa.DSA_OK
+A = 4096  # an aligned address that no refused call reads
+
+
+def norm(**kw):
+    a = dict(x=A, ld_x=64, res=None, ld_res=0, w=A, rows=4, cols=64, dtype=0, eps=1e-6, y=A, ld_y=64, ro=None, ld_ro=0, codes=None,
+             scale=None, group=0, rstd=None)
+    a.update(kw)
+    return dsa._lib.dsa_rmsnorm(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=0, x=None), OK), (dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(dtype=3), INVALID), (dict(dtype=-1), INVALID),
+    (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID), (dict(x=None), INVALID),
+    (dict(w=None), INVALID), (dict(y=None), INVALID), (dict(codes=A), INVALID), (dict(scale=A), INVALID),
+    (dict(codes=A, scale=A, group=64), INVALID), (dict(ld_x=63), INVALID), (dict(ld_y=63), INVALID), (dict(res=A, ld_res=8), INVALID),
+    (dict(ro=A, ld_ro=8), INVALID), (dict(x=A + 1), INVALID), (dict(dtype=2, x=A + 2), INVALID), (dict(codes=A, scale=A + 2), INVALID),
+    (dict(rows=1 << 31), UNSUPPORTED)])
+def test_rmsnorm_refusals(kw, want):
+    assert norm(**kw) == want
+
+
+def norm_bwd(**kw):
+    a = dict(dy=A, ld_dy=64, h=A, ld_h=64, w=A, rstd=A, dres=None, ld_dres=0, rows=4, cols=64, dtype=0, dh=A, ld_dh=64, dw=A, ws=A,
+             size=1 << 20)
+    a.update(kw)
+    return dsa._lib.dsa_rmsnorm_backward(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(dtype=7), INVALID), (dict(dy=None), INVALID), (dict(h=None), INVALID),
+    (dict(w=None), INVALID), (dict(rstd=None), INVALID), (dict(dh=None), INVALID), (dict(dw=None), INVALID), (dict(ws=None), INVALID),
+    (dict(ws=A + 8), INVALID), (dict(ld_dy=1), INVALID), (dict(ld_h=1), INVALID), (dict(ld_dh=1), INVALID),
+    (dict(dres=A, ld_dres=3), INVALID), (dict(h=A + 1), INVALID), (dict(size=4 * 64 * 4 - 1), SMALL), (dict(rows=1 << 31), UNSUPPORTED)])
+def test_rmsnorm_backward_refusals(kw, want):
+    assert norm_bwd(**kw) == want
+
+
+def test_rmsnorm_backward_workspace_grows_to_a_limit():
+    f = dsa.dsa_rmsnorm_backward_workspace_size
+    assert f(0, 64) == 0 and f(4, 0) == 0
+    assert f(4, 64) >= 4 * 64 * 4 and f(10 ** 6, 64) == f(10 ** 9, 64)
+
+
+def rope(**kw):
+    a = dict(x=A, xr=512, xh=128, out=2 * A, orow=512, oh=128, rows=3, heads=4, dim=128, off=0, rot=64, layout=0, dtype=0, pos=A,
+             freqs=A, m=1.0, t=0)
+    a.update(kw)
+    return dsa._lib.dsa_rope(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=0, x=None), OK), (dict(heads=0, x=None), OK), (dict(rows=-1), INVALID), (dict(heads=-1), INVALID), (dict(dim=0), INVALID),
+    (dict(rot=63), INVALID), (dict(rot=0), INVALID), (dict(off=65), INVALID), (dict(off=-1), INVALID), (dict(rot=130), INVALID),
+    (dict(layout=2), INVALID), (dict(dtype=3), INVALID), (dict(m=float("inf")), INVALID), (dict(x=None), INVALID), (dict(out=None), INVALID),
+    (dict(pos=None), INVALID), (dict(freqs=None), INVALID), (dict(freqs=A + 4), INVALID), (dict(x=A + 1), INVALID), (dict(xh=127), INVALID),
+    (dict(oh=127), INVALID), (dict(xr=100), INVALID), (dict(out=A, oh=256), INVALID), (dict(out=A, orow=1024), INVALID),
+    (dict(rows=1 << 31), UNSUPPORTED), (dict(dim=2048, xh=2048, oh=2048, xr=8192, orow=8192, rot=1026), UNSUPPORTED)])
+def test_rope_refusals(kw, want):
+    assert rope(**kw) == want
+
+
+@pytest.mark.parametrize("scaling,name", [(0, "plain"), (1, "linear"), (2, "ntk"), (3, "yarn")])
+@pytest.mark.parametrize("rot,theta,factor,ctx", [(64, 10000.0, 40.0, 4096.0), (4, 500.0, 1.0, 100.0), (128, 1e6, 3.5, 32768.0)])
+def test_rope_frequencies_match_the_oracle(scaling, name, rot, theta, factor, ctx):
+    got, m = dsa.dsa_rope_frequencies(rot, theta, scaling, factor, ctx)
+    want, wm = oracle.rope_frequencies(rot, theta, name, factor, ctx)
+    assert got.dtype == torch.float64 and got.shape == (rot // 2,)
+    assert np.allclose(got.numpy(), want, rtol=1e-14, atol=0) and np.isclose(m, wm, rtol=2.0 ** -24)
+
+
+@pytest.mark.parametrize("args", [(0, 1e4), (7, 1e4), (64, 1.0), (64, float("nan")), (64, 1e4, 4), (64, 1e4, -1), (64, 1e4, 1, 0.5),
+                                  (2, 1e4, 2, 2.0), (64, 1e4, 3, 2.0, 0.0), (64, 1e4, 3, 2.0, 4096.0, 1.0, 2.0),
+                                  (64, 1e4, 3, 2.0, 4096.0, 32.0, 0.0), (64, 1e4, 3, float("inf"), 4096.0)])
+def test_rope_frequencies_refusals(args):
+    with pytest.raises(dsa.DSAError) as e:
+        dsa.dsa_rope_frequencies(*args)
+    assert e.value.status == INVALID
+
+
+def test_rope_frequencies_read_only_what_their_scaling_needs():
+    assert dsa.dsa_rope_frequencies(64, 1e4, dsa.DSA_ROPE_PLAIN, factor=0.0)[1] == 1.0
+    dsa.dsa_rope_frequencies(64, 1e4, dsa.DSA_ROPE_LINEAR, 2.0, original_ctx=-1.0, beta_slow=0.0)
+
+
+def paged(**kw):
+    a = dict(kind=dsa.DSA_KV_PAGED, data=A, scale=A, cu=None, table=A, ctx=A, total=0, max_seqlen=640, blocks=20, size=64, per=10)
+    a.update(kw)
+    return dsa.KVDesc(*a.values())
+
+
+def flat(**kw):
+    return paged(**{**dict(kind=dsa.DSA_KV_CONTIGUOUS, cu=A, table=None, ctx=None, total=100, max_seqlen=100, blocks=0, size=0, per=0), **kw})
+
+
+def append(latent=paged(), keys=paged(), **kw):
+    a = dict(kv=A, ld_kv=576, w=A, eps=1e-6, key=A, ld_key=128, d_i=128, seq=A, pos=A, rows=2, B=2, freqs=A, m=1.0, layout=0, key_layout=1,
+             rot0=0)
+    a.update(kw)
+    ref = lambda d: None if d is None else ctypes.byref(d)  # noqa: E731
+    return dsa._lib.dsa_cache_append(*a.values(), ref(latent), ref(keys), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=0), OK), (dict(rows=-1), INVALID), (dict(B=0), INVALID), (dict(kv=None), INVALID), (dict(key=None), INVALID),
+    (dict(latent=None), INVALID), (dict(keys=None), INVALID), (dict(kv=None, latent=None, key=None, keys=None), INVALID),
+    (dict(w=None), INVALID), (dict(pos=None), INVALID), (dict(freqs=None), INVALID), (dict(freqs=A + 4), INVALID), (dict(kv=A + 8), INVALID),
+    (dict(ld_kv=580), INVALID), (dict(ld_kv=568), INVALID), (dict(key=A + 2), INVALID), (dict(ld_key=129), INVALID), (dict(ld_key=64), INVALID),
+    (dict(d_i=96), UNSUPPORTED), (dict(rot0=1), INVALID), (dict(rot0=66), INVALID), (dict(rot0=-2), INVALID), (dict(d_i=64, rot0=2), INVALID),
+    (dict(layout=2), INVALID), (dict(key_layout=2), INVALID), (dict(eps=-1.0), INVALID), (dict(m=float("nan")), INVALID),
+    (dict(latent=paged(size=32)), UNSUPPORTED), (dict(latent=paged(data=None)), INVALID), (dict(latent=paged(data=A + 8)), INVALID),
+    (dict(keys=paged(scale=None)), INVALID), (dict(keys=paged(data=A + 1)), INVALID), (dict(keys=paged(table=None)), INVALID),
+    (dict(latent=paged(blocks=0)), INVALID), (dict(latent=paged(max_seqlen=0)), INVALID), (dict(latent=flat(cu=None)), INVALID),
+    (dict(latent=flat(total=0)), INVALID), (dict(latent=paged(kind=5)), INVALID), (dict(rows=1 << 31), UNSUPPORTED)])
+def test_cache_append_refusals(kw, want):
+    assert append(**kw) == want
+
+
+def window_prefill(latent=flat(), **kw):
+    a = dict(q=A, latent=ctypes.byref(latent), B=1, H=128, window=8, sinks=0, sm=0.04, out=A, lse=A)
+    a.update(kw)
+    return dsa._lib.dsa_window_mla_prefill(*a.values(), None)
+
+
+def window_decode(latent=paged(), **kw):
+    a = dict(q=A, latent=ctypes.byref(latent), B=2, H=128, window=1000, sinks=0, sm=0.04, out=A, lse=A, ws=A, size=1 << 30)
+    a.update(kw)
+    return dsa._lib.dsa_window_mla_decode(*a.values(), None)
+
+
+COMMON = [(dict(q=None), INVALID), (dict(out=None), INVALID), (dict(latent=None), INVALID), (dict(B=0), INVALID), (dict(H=0), UNSUPPORTED),
+          (dict(H=129), UNSUPPORTED), (dict(window=0), INVALID), (dict(sinks=-1), INVALID), (dict(sm=-0.1), INVALID),
+          (dict(sm=float("nan")), INVALID), (dict(sm=float("inf")), INVALID), (dict(q=A + 8), INVALID), (dict(out=A + 8), INVALID),
+          (dict(lse=A + 2), INVALID)]
+
+
+@pytest.mark.parametrize("kw,want", COMMON)
+def test_window_refusals(kw, want):
+    for call in (window_prefill, window_decode):
+        if "latent" in kw:
+            assert dsa._lib.dsa_window_mla_prefill(A, None, 1, 128, 8, 0, 0.04, A, A, None) == want
+            assert dsa._lib.dsa_window_mla_decode(A, None, 1, 128, 8, 0, 0.04, A, A, A, 1 << 30, None) == want
+        else:
+            assert call(**kw) == want
+
+
+def test_window_descriptor_refusals():
+    assert window_prefill(paged()) == INVALID and window_decode(flat()) == INVALID
+    assert window_prefill(flat(data=A + 8)) == INVALID and window_prefill(flat(total=0)) == INVALID
+    assert window_prefill(flat(max_seqlen=0)) == INVALID and window_prefill(flat(total=1 << 25)) == UNSUPPORTED
+    assert window_decode(paged(size=32)) == UNSUPPORTED and window_decode(paged(max_seqlen=641)) == INVALID
+    assert window_decode(paged(table=None)) == INVALID and window_decode(paged(ctx=None)) == INVALID
+    assert window_decode(paged(blocks=1 << 25)) == UNSUPPORTED
+
+
+def test_window_decode_workspace():
+    f = dsa.dsa_window_mla_workspace_size
+    assert f(0, 128, 8, 0, 100) == 0 and f(4, 128, 0, 0, 100) == 0 and f(4, 128, 8, 0, 0) == 0
+    assert f(1, 128, 64, 0, 100000) == 0          # one 64-key chunk: nothing to split
+    assert f(64, 128, 100, 4, 100000) == 0        # few chunks and the sequences nearly fill the GPU
+    big = f(1, 128, 131072, 0, 131072)
+    assert big == 74 * 128 * 512 * 4 + 74 * 128 * 2 * 4   # one unit per CTA pair
+    assert f(1, 128, 2 ** 31 - 1, 2 ** 31 - 1, 131072) == big
+    d = paged(max_seqlen=640)
+    need = f(2, 128, 1000, 0, 640)
+    assert need > 0
+    assert window_decode(d, size=need - 1) == SMALL and window_decode(d, ws=None) == INVALID and window_decode(d, ws=A + 128) == INVALID
+
+
+def test_wrappers_refuse_tensors_they_cannot_pass_on():
+    x, w = torch.zeros(4, 8), torch.zeros(8)
+    pos, freqs = torch.zeros(4, dtype=torch.int32), torch.zeros(32, dtype=torch.float64)
+    with pytest.raises(ValueError):
+        dsa.dsa_rmsnorm(x, w, 1e-6, y=x)                                     # not on a GPU
+    with pytest.raises(ValueError):
+        dsa.dsa_rmsnorm_backward(x, x, w, w, x, w, w)
+    with pytest.raises(ValueError):
+        dsa.dsa_rope(x.view(4, 1, 8), pos, freqs, x.view(4, 1, 8), 0, 8)
+    with pytest.raises(ValueError):
+        dsa.dsa_cache_append(None, None, 0.0, x.bfloat16(), None, pos, freqs, None, None)
+    lat = dsa.contiguous_desc(torch.zeros(4, 576, dtype=torch.bfloat16), torch.tensor([0, 4], dtype=torch.int32), 4)
+    q, out = torch.zeros(4, 16, 576, dtype=torch.bfloat16), torch.zeros(4, 16, 512, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        dsa.dsa_window_mla_prefill(q, lat, 1, 16, 4, 0, 0.04, out)
+    with pytest.raises(ValueError):
+        dsa.dsa_window_mla_decode(q, lat, 4, 16, 4, 0, 0.04, out)
