@@ -283,67 +283,95 @@ dsa_status with_dtype(int32_t dtype, F f) {
 // Whether a [rows, cols] operand (null: absent) can be read in aligned pieces of 8 elements.
 bool wide(const void* p, int64_t ld) { return p == nullptr || (aligned(p, 16) && ld % 8 == 0); }
 
-// Pieces of 8 elements per thread and threads per row for a CTA-wide row: at least 2 pieces per
-// thread (two 16-byte loads in flight each) where that leaves at most max_threads.
-void row_shape(int cols, int max_threads, int min_pieces, int* pieces, int* threads) {
-  const int n = cols / 8;
-  int ch = min_pieces;
-  while (ch < 4 && (n + ch - 1) / ch > max_threads) ch *= 2;
-  *pieces = ch;
-  *threads = ((n + ch - 1) / ch + 31) / 32 * 32;
+// Threads for a CTA-wide row of n pieces, ch per thread.
+int row_threads(int n, int ch) { return ((n + ch - 1) / ch + 31) / 32 * 32; }
+
+template <typename T, int V, int CH, bool WARP>
+dsa_status launch_rmsnorm_v(const NormParams& p, cudaStream_t s) {
+  const unsigned rows = static_cast<unsigned>(p.rows);
+  if constexpr (WARP) rmsnorm_kernel<T, V, CH, true><<<(rows + norm::kWarpRows - 1) / norm::kWarpRows, norm::kWarpRows * 32, 0, s>>>(p);
+  else rmsnorm_kernel<T, V, CH, false><<<rows, row_threads((p.cols + V - 1) / V, CH), 0, s>>>(p);
+  return launch_status();
 }
 
 template <typename T>
 dsa_status launch_rmsnorm(const NormParams& p, bool vector, cudaStream_t s) {
-  const unsigned rows = static_cast<unsigned>(p.rows);
-  if (!vector || p.cols > 4 * 8 * 1024) {
-    rmsnorm_general_kernel<T><<<rows, norm::kGeneralThreads, 0, s>>>(p);
-    return launch_status();
+  const int n = p.cols / 8;
+  if (vector) {
+    if (n <= 32) return launch_rmsnorm_v<T, 8, 1, true>(p, s);
+    if (n <= 64) return launch_rmsnorm_v<T, 8, 2, true>(p, s);
+    if (n <= 128) return launch_rmsnorm_v<T, 8, 4, true>(p, s);
+    // few rows: as many threads as there are pieces; many: two loads in flight per thread
+    if (n <= 1024 && p.rows <= kSms) return launch_rmsnorm_v<T, 8, 1, false>(p, s);
+    if (n <= 2 * 1024) return launch_rmsnorm_v<T, 8, 2, false>(p, s);
+    if (n <= 4 * 1024) return launch_rmsnorm_v<T, 8, 4, false>(p, s);
+  } else {
+    if (p.cols <= 128) return launch_rmsnorm_v<T, 1, 4, true>(p, s);
+    if (p.cols <= 256) return launch_rmsnorm_v<T, 1, 8, true>(p, s);
+    if (p.cols <= 512) return launch_rmsnorm_v<T, 1, 16, true>(p, s);
+    if (p.cols <= 1024) return launch_rmsnorm_v<T, 1, 32, true>(p, s);
+    if (p.cols <= 8 * 1024) return launch_rmsnorm_v<T, 1, 8, false>(p, s);
+    if (p.cols <= 16 * 1024) return launch_rmsnorm_v<T, 1, 16, false>(p, s);
   }
-  if (p.cols <= norm::kWarpCols) {
-    const unsigned grid = (rows + norm::kWarpRows - 1) / norm::kWarpRows;
-    const int ch = (p.cols + 255) / 256;
-    if (ch <= 1) rmsnorm_kernel<T, 1, true><<<grid, norm::kWarpRows * 32, 0, s>>>(p);
-    else if (ch <= 2) rmsnorm_kernel<T, 2, true><<<grid, norm::kWarpRows * 32, 0, s>>>(p);
-    else rmsnorm_kernel<T, 4, true><<<grid, norm::kWarpRows * 32, 0, s>>>(p);
-    return launch_status();
-  }
-  int ch, threads;
-  row_shape(p.cols, 1024, p.rows <= kSms ? 1 : 2, &ch, &threads);
-  if (ch == 1) rmsnorm_kernel<T, 1, false><<<rows, threads, 0, s>>>(p);
-  else if (ch == 2) rmsnorm_kernel<T, 2, false><<<rows, threads, 0, s>>>(p);
-  else rmsnorm_kernel<T, 4, false><<<rows, threads, 0, s>>>(p);
+  rmsnorm_general_kernel<T><<<static_cast<unsigned>(p.rows), norm::kGeneralThreads, 0, s>>>(p);
   return launch_status();
 }
 
-// CTAs of the backward (each writes one row of partial sums of dw).
-constexpr int kNormBwdCtas = 4 * kSms;
-int64_t norm_bwd_ctas(int64_t rows) { return rows < kNormBwdCtas ? rows : kNormBwdCtas; }
+// CTAs of the backward, each of which writes one row of partial sums of dw: enough per SM to hide
+// a row's reduction (about 4K columns between them), at most one per row.
+int norm_bwd_per_sm(int cols) { return std::min(std::max(4096 / cols, 1), 8); }
+int64_t norm_bwd_ctas(int64_t rows, int cols) {
+  const int64_t most = static_cast<int64_t>(kSms) * norm_bwd_per_sm(cols);
+  return rows < most ? rows : most;
+}
 
-template <typename T>
-dsa_status launch_rmsnorm_backward(const NormBwdParams& p, bool vector, float* dw, cudaStream_t s) {
-  const int64_t most = norm_bwd_ctas(p.rows);
-  unsigned grid;
-  if (!vector || p.cols > 4 * 8 * 512) {
-    grid = static_cast<unsigned>(most);
-    rmsnorm_backward_general_kernel<T><<<grid, norm::kGeneralThreads, 0, s>>>(p);
-  } else if (p.cols <= norm::kWarpCols) {
-    grid = static_cast<unsigned>(std::min<int64_t>(most, (p.rows + norm::kWarpRows - 1) / norm::kWarpRows));
-    const int ch = (p.cols + 255) / 256;
-    if (ch <= 1) rmsnorm_backward_kernel<T, 1, true><<<grid, norm::kWarpRows * 32, 0, s>>>(p);
-    else if (ch <= 2) rmsnorm_backward_kernel<T, 2, true><<<grid, norm::kWarpRows * 32, 0, s>>>(p);
-    else rmsnorm_backward_kernel<T, 4, true><<<grid, norm::kWarpRows * 32, 0, s>>>(p);
+template <typename T, int V, int CH, bool WARP>
+dsa_status launch_rmsnorm_backward_v(const NormBwdParams& p, float* dw, cudaStream_t s) {
+  int64_t ctas = norm_bwd_ctas(p.rows, p.cols);
+  if constexpr (WARP) {
+    ctas = std::min<int64_t>(std::min<int64_t>(ctas, 4 * kSms), (p.rows + norm::kWarpRows - 1) / norm::kWarpRows);
+    rmsnorm_backward_kernel<T, V, CH, true><<<static_cast<unsigned>(ctas), norm::kWarpRows * 32, 0, s>>>(p);
   } else {
-    grid = static_cast<unsigned>(most);
-    int ch, threads;
-    row_shape(p.cols, 512, 1, &ch, &threads);
-    if (ch == 1) rmsnorm_backward_kernel<T, 1, false><<<grid, threads, 0, s>>>(p);
-    else if (ch == 2) rmsnorm_backward_kernel<T, 2, false><<<grid, threads, 0, s>>>(p);
-    else rmsnorm_backward_kernel<T, 4, false><<<grid, threads, 0, s>>>(p);
+    rmsnorm_backward_kernel<T, V, CH, false>
+        <<<static_cast<unsigned>(ctas), row_threads((p.cols + V - 1) / V, CH), 0, s>>>(p);
   }
   const dsa_status st = launch_status();
   if (st != DSA_OK) return st;
-  rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 256, 0, s>>>(p.part, static_cast<int>(grid), p.cols, dw);
+  rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 256, 0, s>>>(p.part, static_cast<int>(ctas), p.cols, dw);
+  return launch_status();
+}
+
+template <typename T>
+dsa_status launch_rmsnorm_backward(const NormBwdParams& p, bool vector, float* dw, cudaStream_t s) {
+  const int n = p.cols / 8;
+  if (vector) {
+    if (n <= 32) return launch_rmsnorm_backward_v<T, 8, 1, true>(p, dw, s);
+    if (n <= 64) return launch_rmsnorm_backward_v<T, 8, 2, true>(p, dw, s);
+    const int64_t stage = static_cast<int64_t>(p.cols) * sizeof(T) * (p.dres != nullptr ? 3 : 2);
+    const int stages = static_cast<int>(std::min<int64_t>(norm::kRingBytes / norm_bwd_per_sm(p.cols) / stage, norm::kRingMax));
+    if (n <= 1024 && stages >= 2) {
+      const int64_t ctas = norm_bwd_ctas(p.rows, p.cols);
+      const int smem = static_cast<int>(stages * stage);
+      if (cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return DSA_ERR_CUDA;
+      rmsnorm_backward_ring_kernel<T><<<static_cast<unsigned>(ctas), row_threads(n, 1), smem, s>>>(p, stages);
+      const dsa_status st = launch_status();
+      if (st != DSA_OK) return st;
+      rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 256, 0, s>>>(p.part, static_cast<int>(ctas), p.cols, dw);
+      return launch_status();
+    }
+    if (n <= 2 * 1024) return launch_rmsnorm_backward_v<T, 8, 2, false>(p, dw, s);
+  } else {
+    if (p.cols <= 128) return launch_rmsnorm_backward_v<T, 1, 4, true>(p, dw, s);
+    if (p.cols <= 512) return launch_rmsnorm_backward_v<T, 1, 16, true>(p, dw, s);
+    if (p.cols <= 4 * 1024) return launch_rmsnorm_backward_v<T, 1, 4, false>(p, dw, s);
+    if (p.cols <= 8 * 1024) return launch_rmsnorm_backward_v<T, 1, 8, false>(p, dw, s);
+  }
+  const int64_t ctas = norm_bwd_ctas(p.rows, p.cols);
+  rmsnorm_backward_general_kernel<T><<<static_cast<unsigned>(ctas), norm::kGeneralThreads, 0, s>>>(p);
+  const dsa_status st = launch_status();
+  if (st != DSA_OK) return st;
+  rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 256, 0, s>>>(p.part, static_cast<int>(ctas), p.cols, dw);
   return launch_status();
 }
 
@@ -351,34 +379,36 @@ template <typename T>
 dsa_status launch_rope(RopeParams p, bool vector, cudaStream_t s) {
   const int pairs = p.rot / 2;
   const int rest = p.copy_rest ? p.dim - p.rot : 0;
-  if (vector) p.items_per_head = p.rot / (p.half_layout ? 16 : 8) + rest / 8;
-  else p.items_per_head = pairs + rest;
-  // A CTA moves about kUnroll items per thread: several rows when a row has fewer, a range of a
-  // row's heads when it has more (each range forms its own table: rot / 2 entries).
-  const int64_t target = rope::kThreads * (vector ? rope::kUnroll : 8);
-  const int64_t per_row = static_cast<int64_t>(p.heads) * p.items_per_head;
+  if (vector) p.items = p.rot / (p.half_layout ? 16 : 8) + rest / 8;
+  else p.items = pairs + rest;
+  p.lanes = std::min(p.items, rope::kThreads);
+  // groups per CTA: as many as fit, but a divisor of the heads when that costs less than half
+  p.groups = rope::kThreads / p.lanes;
+  for (int g = p.groups; 2 * g > p.groups; --g)
+    if (p.heads % g == 0) {
+      p.groups = g;
+      break;
+    }
+  // A CTA walks one batch of (row, head) pairs: several rows when a row has fewer, a range of a row's
+  // heads when it has more (each CTA makes its own table of rot / 2 entries per row).
+  const int batch = p.groups * rope::unroll<T>();
   int64_t parts = 1;
   p.rows_per_cta = 1;
   p.heads_per_cta = p.heads;
-  if (per_row >= 2 * target) {
-    p.heads_per_cta = static_cast<int32_t>(std::max<int64_t>(1, target / p.items_per_head));
+  if (p.heads >= 2 * batch) {
+    p.heads_per_cta = static_cast<int32_t>(std::max<int64_t>(batch, (p.heads + 65534) / 65535));
     parts = (p.heads + p.heads_per_cta - 1) / p.heads_per_cta;
-    if (parts > 65535) {
-      parts = 65535;
-      p.heads_per_cta = static_cast<int32_t>((p.heads + parts - 1) / parts);
-      parts = (p.heads + p.heads_per_cta - 1) / p.heads_per_cta;
-    }
   } else {
-    int64_t r = std::min<int64_t>(target / per_row, rope::kTable / pairs);
-    // few rows: spread them over the GPU first
-    r = std::min<int64_t>(r, (p.rows + kSms - 1) / kSms);
+    int64_t r = std::min<int64_t>(batch / p.heads, rope::kTable / pairs);
+    r = std::min<int64_t>(r, (p.rows + kSms - 1) / kSms);  // few rows: over the GPU first
     p.rows_per_cta = static_cast<int32_t>(std::max<int64_t>(1, r));
   }
   const int64_t ctas = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
   const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(parts));
-  if (!vector) rope_general_kernel<T><<<grid, rope::kThreads, 0, s>>>(p);
-  else if (p.half_layout) rope_kernel<T, true><<<grid, rope::kThreads, 0, s>>>(p);
-  else rope_kernel<T, false><<<grid, rope::kThreads, 0, s>>>(p);
+  const int threads = (p.groups * p.lanes + 31) / 32 * 32;
+  if (!vector) rope_kernel<T, 1, false><<<grid, threads, 0, s>>>(p);
+  else if (p.half_layout) rope_kernel<T, 8, true><<<grid, threads, 0, s>>>(p);
+  else rope_kernel<T, 8, false><<<grid, threads, 0, s>>>(p);
   return launch_status();
 }
 
@@ -391,13 +421,14 @@ dsa_status append_cache(const dsa_kv_desc* d, bool with_scale, size_t align, App
   c->max_seqlen = d->max_seqlen;
   if (d->kind == DSA_KV_CONTIGUOUS) {
     if (d->cu_seqlens == nullptr || d->total_tokens <= 0) return DSA_ERR_INVALID_ARGUMENT;
+    if (d->total_tokens > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
     c->cu = d->cu_seqlens;
-    c->rows = d->total_tokens;
+    c->rows = static_cast<int32_t>(d->total_tokens);
     return DSA_OK;
   }
   if (d->kind != DSA_KV_PAGED || d->block_table == nullptr || d->num_blocks <= 0 || d->max_blocks_per_seq <= 0)
     return DSA_ERR_INVALID_ARGUMENT;
-  if (d->block_size != 64) return DSA_ERR_UNSUPPORTED;
+  if (d->block_size != 64 || static_cast<int64_t>(d->num_blocks) * 64 > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
   c->table = d->block_table;
   c->rows = d->num_blocks;
   c->max_blocks = d->max_blocks_per_seq;
@@ -986,7 +1017,7 @@ dsa_status dsa_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_
 
 size_t dsa_rmsnorm_backward_workspace_size(int64_t rows, int32_t cols) {
   if (rows <= 0 || cols <= 0) return 0;
-  return align256(static_cast<size_t>(norm_bwd_ctas(rows)) * cols * sizeof(float));
+  return align256(static_cast<size_t>(norm_bwd_ctas(rows, cols)) * cols * sizeof(float));
 }
 
 dsa_status dsa_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* weight,
@@ -1155,9 +1186,11 @@ dsa_status dsa_cache_append(const void* kv, int64_t ld_kv, const void* kv_weight
   p.half = layout == DSA_ROPE_HALF;
   p.key_half = key_layout == DSA_ROPE_HALF;
   p.key_rot0 = key_rot_offset;
-  const unsigned grid = static_cast<unsigned>((rows + append::kWarps - 1) / append::kWarps);
-  if (keys != nullptr && d_I == 64) cache_append_kernel<64><<<grid, append::kWarps * 32, 0, as_stream(stream)>>>(p);
-  else cache_append_kernel<128><<<grid, append::kWarps * 32, 0, as_stream(stream)>>>(p);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((rows + append::kWarps - 1) / append::kWarps, kSms * append::kCtas));
+  auto launch = [&](auto kern) { kern<<<grid, append::kWarps * 32, 0, as_stream(stream)>>>(p); };
+  if (keys == nullptr) launch(cache_append_kernel<true, 0>);
+  else if (latent == nullptr) launch(d_I == 64 ? cache_append_kernel<false, 64> : cache_append_kernel<false, 128>);
+  else launch(d_I == 64 ? cache_append_kernel<true, 64> : cache_append_kernel<true, 128>);
   return launch_status();
 }
 

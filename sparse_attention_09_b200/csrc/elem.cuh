@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "sm100.cuh"
 
 namespace dsa {
 namespace elem {
@@ -99,6 +100,30 @@ __device__ __forceinline__ void Raw8<float>::set(const float* f) {
   for (int i = 0; i < 2; ++i)
     v[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
                       __float_as_uint(f[4 * i + 3]));
+}
+
+// V = 8 or 1 consecutive elements of a row.
+template <typename T, int V>
+struct Piece : Raw8<T> {
+  static_assert(V == 8, "pieces hold 8 elements or 1");
+};
+template <typename T>
+struct Piece<T, 1> {
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void zero() { v = from_f32<T>(0.f); }
+  __device__ __forceinline__ void store(T* p) const { *p = v; }
+  __device__ __forceinline__ void get(float* f) const { f[0] = to_f32(v); }
+  __device__ __forceinline__ void set(const float* f) { v = from_f32<T>(f[0]); }
+};
+
+// Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) from global to this CTA's
+// shared memory; its bytes count towards the barrier's phase.
+__device__ __forceinline__ void bulk_load(void* dst_smem, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   dev::smem_addr(dst_smem)),
+               "l"(src), "r"(bytes), "r"(dev::smem_addr(bar))
+               : "memory");
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

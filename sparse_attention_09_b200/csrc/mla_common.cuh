@@ -42,6 +42,11 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// Copies 16 bytes, or writes 16 zero bytes without reading src (which still names mapped memory).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst_smem, const void* src, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "r"(copy ? 16 : 0) : "memory");
+}
+
 // Number of 64-entry chunks up to the last valid (>= 0) index of a selection row, computed by
 // one warp (all roles compute it the same way from the same row).
 __device__ __forceinline__ int active_chunks(const int32_t* row, int k) {

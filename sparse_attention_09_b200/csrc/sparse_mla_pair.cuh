@@ -291,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
   if ((warp >= kFirstProducerWarp && warp < kFirstProducerWarp + kProducerWarps) || (warp >= kVWarp0 && warp < kVWarp0 + 2)) {
     const bool kqrole = warp < kVWarp0;
     auto copy16 = [](uint32_t dst, const void* src, int kr) {
-      if constexpr (WINDOW) cp_async16_or_zero(dst, src, kr >= 0);
+      if constexpr (WINDOW) mla::cp_async16_or_zero(dst, src, kr >= 0);
       else cp_async16(dst, src);
     };
     // ================= gather producers =================

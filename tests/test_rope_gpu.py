@@ -1,8 +1,9 @@
 """dsa_rope against the float64 oracle.
 
 Tolerance, from the arithmetic: the fraction of a turn is rounded to fp32 once (at most 2^-26 turns, 2^-23.3
-rad), sincospif is good to about 2 units in the last place (2^-23), and two products and a sum round three
-times: 2^-20 of mscale (|a| + |b|) on each rotated element, beside half a unit of the output type."""
+rad) and, for 16-bit tensors, once more in radians (2^-23.3); the sine is good to about 2 units in the last place
+(2^-23, fp32 tensors) or 2^-21.2 absolute (16-bit ones), and two products and a sum round three times: together
+under 2^-20 of mscale (|a| + |b|) on each rotated element, beside half a unit of the output type."""
 import numpy as np
 import pytest
 import torch
