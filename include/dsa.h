@@ -504,20 +504,22 @@ dsa_status dsa_cache_append(const void* kv, int64_t ld_kv, const void* kv_weight
  *   prefill: latent contiguous, queries are the packed tokens [0, cu_seqlens[B]); rows of out and lse
  *     behind the last sequence are left as they were.
  *   decode: latent paged, one query per sequence at position ctx - 1, ctx = context_lens[b] clamped
- *     to [0, latent->max_seqlen] (clamping sets DSA_ERR_DEVICE_CHECK).  The visible keys are split
- *     over the GPU when the sequences alone do not fill it; the parts go to `workspace`
- *     (256-byte aligned, dsa_window_mla_workspace_size bytes; may be NULL where that is 0) and are merged
- *     by log-sum-exp.  Keys in blocks outside the pool are masked and set DSA_ERR_DEVICE_CHECK.
+ *     to [0, latent->max_seqlen] (clamping sets DSA_ERR_DEVICE_CHECK).  When the sequences
+ *     alone do not fill the GPU evenly, the chunks of all of them are shared out over it, whatever
+ *     their lengths; the parts of split sequences go to `workspace` (256-byte aligned,
+ *     dsa_window_mla_workspace_size bytes; may be NULL where that is 0) and are merged by log-sum-exp.
+ *     Calls that may overlap on the GPU need workspaces of their own.  Keys in blocks outside the pool are masked and set DSA_ERR_DEVICE_CHECK.
  * Forward only, like every attention of this library.  1 <= H <= 128 (64-head tiles: small H costs as
- * much as 128).  DSA_ERR_INVALID_ARGUMENT: as dsa_sparse_mla_*, window < 1, sinks < 0, sm_scale negative
- * or not finite; DSA_ERR_UNSUPPORTED: H, the page size, or sizes beyond 2^31 - 1 rows.
+ * much as 128).  DSA_ERR_INVALID_ARGUMENT: as dsa_sparse_mla_*, window < 1, sinks < 0, sm_scale not
+ * positive and finite; DSA_ERR_UNSUPPORTED: H, the page size, or sizes beyond 2^31 - 1 rows.
  */
 dsa_status dsa_window_mla_prefill(const void* q, const dsa_kv_desc* latent, int32_t B, int32_t H, int32_t window,
                                   int32_t sinks, float sm_scale, void* out, float* lse, void* stream);
 dsa_status dsa_window_mla_decode(const void* q, const dsa_kv_desc* latent, int32_t B, int32_t H, int32_t window,
                                  int32_t sinks, float sm_scale, void* out, float* lse, void* workspace,
                                  size_t ws_bytes, void* stream);
-/* Workspace bytes of dsa_window_mla_decode (max_ctx = latent->max_seqlen; 0 when nothing is split). */
+/* Workspace bytes of dsa_window_mla_decode (max_ctx = latent->max_seqlen; 0 when each sequence is
+ * worked on whole). */
 size_t dsa_window_mla_workspace_size(int32_t B, int32_t H, int32_t window, int32_t sinks, int32_t max_ctx);
 
 #ifdef __cplusplus

@@ -26,6 +26,7 @@
 #include "rope.cuh"
 #include "sparse_mla_pair.cuh"
 #include "topk.cuh"
+#include "window_mla.cuh"
 
 namespace dsa {
 namespace {
@@ -223,16 +224,16 @@ int decode_splits(int B, int k) {
   return s;
 }
 
-// Sparse, masked and window prefill, and decode: the head-split pair kernel.  Q is read by TMA as a
+// Sparse prefill, masked prefill and decode: the head-split pair kernel.  Q is read by TMA as a
 // [q_rows * H, 576] bf16 matrix in 64 x 64 tiles (128-byte swizzle).
-template <bool DECODE, int FORM = kMlaSparse>
+template <bool DECODE, bool MASKED = false>
 dsa_status launch_mla_pair(const void* latent, const void* q, int64_t q_rows, const MlaParams& p, int64_t units,
                            cudaStream_t s) {
   CUtensorMap qm;
   if (!make_map_2d(&qm, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kLatentDim, static_cast<uint64_t>(q_rows) * p.H,
                    kLatentDim * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
     return DSA_ERR_INVALID_ARGUMENT;
-  auto kern = sparse_mla_pair_kernel<DECODE, FORM>;
+  auto kern = sparse_mla_pair_kernel<DECODE, MASKED>;
   const int smem = mlap::kSmemBytes + 1024;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return DSA_ERR_CUDA;
@@ -241,27 +242,40 @@ dsa_status launch_mla_pair(const void* latent, const void* q, int64_t q_rows, co
   return launch_status();
 }
 
-// Window decode: splits per sequence.  A unit (sequence, split) costs its 64-key chunks plus about
-// kUnitChunks chunks' time for its Q load, pipeline fill and O readout, and the units run in
-// rounds over the CTA pairs; the split count with the least rounds x (chunks + kUnitChunks) is
-// taken, the smaller of equals (fewer partial results).  Unlike the selection's decode_splits it
-// need not divide anything: the kernel deals a sequence's chunks out evenly.
-constexpr int kUnitChunks = 6;
+// ---- window MLA --------------------------------------------------------------------------------
+// Whether decode shares the chunks of all sequences out over the clusters (and merges the split
+// sequences) instead of giving each cluster whole sequences.  In chunks' times: whole sequences take
+// rounds of (chunks + kUnitCost); shared, the even share, 15 for what a split adds (a second piece of
+// work per cluster, fp32 partial outputs, the merge's launch) and a tenth of the share.  By the longest
+// context the arguments allow: the contexts themselves are on the device.
+// Measured (us, shared / whole): 16 sequences of 1024 keys 27.7 / 28.0, of 2048 31.8 / 46.0; of 4096 keys
+// 32 sequences 66 / 89, 64: 107 / 95, 80: 128 / 177, 128: 190 / 183; 8 of 512 21.5 / 19.4.
+constexpr int kShareSeqs = 1024;  // a cluster's start is found by a scan of the contexts
 
-int window_splits(int B, int window, int sinks, int max_ctx) {
+bool window_shared(int B, int window, int sinks, int max_ctx) {
   const int64_t keys = std::min<int64_t>(max_ctx, static_cast<int64_t>(window) + sinks);
   const int64_t chunks = (keys + 63) / 64;
-  int64_t best = 0;
-  int splits = 1;
-  for (int s = 1; s <= kMlaClusters && s <= std::max<int64_t>(chunks, 1); ++s) {
-    const int64_t rounds = (static_cast<int64_t>(B) * s + kMlaClusters - 1) / kMlaClusters;
-    const int64_t cost = rounds * ((chunks + s - 1) / s + kUnitChunks);
-    if (s == 1 || cost < best) {
-      best = cost;
-      splits = s;
-    }
-  }
-  return splits;
+  if (B > kShareSeqs || chunks < 2) return false;
+  const int64_t whole = (B + kMlaClusters - 1) / kMlaClusters * (chunks + win::kUnitCost);
+  const int64_t share = B * (chunks + win::kUnitCost) / kMlaClusters;
+  return share + share / 10 + 15 < whole;
+}
+
+size_t window_plan_bytes(int B) { return align256((static_cast<size_t>(B) + 2) * sizeof(int64_t)); }
+size_t window_part_bytes(int H) { return align256(static_cast<size_t>(2 * kMlaClusters) * H * kValueDim * 4); }
+
+template <bool DECODE>
+dsa_status launch_window(const void* latent, const void* q, const WinParams& p, int64_t clusters, cudaStream_t s) {
+  CUtensorMap qm;
+  if (!make_map_2d(&qm, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kLatentDim, static_cast<uint64_t>(p.rows) * p.H, kLatentDim * 2,
+                   64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+    return DSA_ERR_INVALID_ARGUMENT;
+  auto kern = window_mla_kernel<DECODE>;
+  const int smem = win::kSmemBytes + 1024;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return DSA_ERR_CUDA;
+  kern<<<static_cast<unsigned>(2 * std::min<int64_t>(clusters, kMlaClusters)), win::kThreads, smem, s>>>(
+      static_cast<const __nv_bfloat16*>(latent), p, qm);
+  return launch_status();
 }
 
 bool mla_shape_ok(int H, int k) { return H >= 1 && H <= 128 && k >= 64 && k <= 2048 && k % 64 == 0; }
@@ -840,7 +854,7 @@ dsa_status dsa_masked_mla_prefill(const void* q, const dsa_kv_desc* latent, cons
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
-  return launch_mla_pair<false, kMlaMasked>(latent->data, q, p.rows, p, p.rows, as_stream(stream));
+  return launch_mla_pair<false, true>(latent->data, q, p.rows, p, p.rows, as_stream(stream));
 }
 
 dsa_status dsa_sparse_mla_decode(const void* q, const dsa_kv_desc* latent, const int32_t* idx, int32_t B, int32_t H,
@@ -882,7 +896,7 @@ dsa_status dsa_sparse_mla_decode(const void* q, const dsa_kv_desc* latent, const
   dsa_status st = launch_mla_pair<true>(latent->data, q, B, p, static_cast<int64_t>(B) * splits, s);
   if (st != DSA_OK) return st;
   if (splits == 1) return DSA_OK;
-  mla_combine_kernel<false><<<dim3(H, B), 128, 0, s>>>(p.part_o, p.part_ml, splits, H, static_cast<__nv_bfloat16*>(out), lse);
+  mla_combine_kernel<<<dim3(H, B), 128, 0, s>>>(p.part_o, p.part_ml, splits, H, static_cast<__nv_bfloat16*>(out), lse);
   return launch_status();
 }
 
@@ -1196,18 +1210,16 @@ dsa_status dsa_cache_append(const void* kv, int64_t ld_kv, const void* kv_weight
 
 // Arguments common to both window entries; fills what they share.
 static dsa_status window_common(const void* q, const dsa_kv_desc* latent, int32_t B, int32_t H, int32_t window,
-                                int32_t sinks, float sm_scale, void* out, float* lse, MlaParams* p) {
+                                int32_t sinks, float sm_scale, void* out, float* lse, WinParams* p) {
   if (q == nullptr || latent == nullptr || latent->data == nullptr || out == nullptr || B <= 0)
     return DSA_ERR_INVALID_ARGUMENT;
   if (!aligned(q, 16) || !aligned(latent->data, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSA_ERR_INVALID_ARGUMENT;
-  if (window < 1 || sinks < 0 || !(sm_scale >= 0.f) || !std::isfinite(sm_scale) || latent->max_seqlen <= 0)
+  if (window < 1 || sinks < 0 || !(sm_scale > 0.f) || !std::isfinite(sm_scale) || latent->max_seqlen <= 0)
     return DSA_ERR_INVALID_ARGUMENT;
   if (H < 1 || H > 128) return DSA_ERR_UNSUPPORTED;
   std::memset(p, 0, sizeof(*p));
-  p->q = static_cast<const __nv_bfloat16*>(q);
   p->B = B;
   p->H = H;
-  p->splits = 1;
   p->window = window;
   p->sinks = sinks;
   p->scale_log2 = sm_scale * 1.4426950408889634f;
@@ -1218,28 +1230,28 @@ static dsa_status window_common(const void* q, const dsa_kv_desc* latent, int32_
 
 dsa_status dsa_window_mla_prefill(const void* q, const dsa_kv_desc* latent, int32_t B, int32_t H, int32_t window,
                                   int32_t sinks, float sm_scale, void* out, float* lse, void* stream) {
-  MlaParams p;
+  WinParams p;
   const dsa_status st = window_common(q, latent, B, H, window, sinks, sm_scale, out, lse, &p);
   if (st != DSA_OK) return st;
   if (latent->kind != DSA_KV_CONTIGUOUS || latent->cu_seqlens == nullptr || latent->total_tokens <= 0)
     return DSA_ERR_INVALID_ARGUMENT;
-  if (latent->total_tokens * H > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
+  if (latent->total_tokens * H > 0x7FFFFFFFLL - 128) return DSA_ERR_UNSUPPORTED;  // row coordinates of 128-row tiles
   p.cu_seqlens = latent->cu_seqlens;
   p.rows = latent->total_tokens;
-  return launch_mla_pair<false, kMlaWindow>(latent->data, q, p.rows, p, p.rows, as_stream(stream));
+  return launch_window<false>(latent->data, q, p, p.rows, as_stream(stream));
 }
 
 size_t dsa_window_mla_workspace_size(int32_t B, int32_t H, int32_t window, int32_t sinks, int32_t max_ctx) {
   if (B <= 0 || H <= 0 || window < 1 || sinks < 0 || max_ctx <= 0) return 0;
-  const int splits = window_splits(B, window, sinks, max_ctx);
-  return splits == 1 ? 0 : decode_partials_bytes(B, H, splits);
+  if (!window_shared(B, window, sinks, max_ctx)) return 0;
+  return window_plan_bytes(B) + window_part_bytes(H) + align256(static_cast<size_t>(2 * kMlaClusters) * H * 2 * 4);
 }
 
 dsa_status dsa_window_mla_decode(const void* q, const dsa_kv_desc* latent, int32_t B, int32_t H, int32_t window,
                                  int32_t sinks, float sm_scale, void* out, float* lse, void* workspace,
                                  size_t ws_bytes, void* stream) {
-  MlaParams p;
-  dsa_status st = window_common(q, latent, B, H, window, sinks, sm_scale, out, lse, &p);
+  WinParams p;
+  const dsa_status st = window_common(q, latent, B, H, window, sinks, sm_scale, out, lse, &p);
   if (st != DSA_OK) return st;
   if (latent->kind != DSA_KV_PAGED || latent->block_table == nullptr || latent->context_lens == nullptr ||
       latent->num_blocks <= 0 || latent->max_blocks_per_seq <= 0)
@@ -1247,27 +1259,28 @@ dsa_status dsa_window_mla_decode(const void* q, const dsa_kv_desc* latent, int32
   if (latent->block_size != 64) return DSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(latent->max_seqlen) > static_cast<int64_t>(latent->max_blocks_per_seq) * 64)
     return DSA_ERR_INVALID_ARGUMENT;
-  if (static_cast<int64_t>(latent->num_blocks) * 64 > 0x7FFFFFFFLL || static_cast<int64_t>(B) * H > 0x7FFFFFFFLL)
+  if (static_cast<int64_t>(latent->num_blocks) * 64 > 0x7FFFFFFFLL || static_cast<int64_t>(B) * H > 0x7FFFFFFFLL - 128)
     return DSA_ERR_UNSUPPORTED;
-  p.splits = window_splits(B, window, sinks, latent->max_seqlen);
-  if (p.splits > 1) {
+  p.shared = window_shared(B, window, sinks, latent->max_seqlen);
+  if (p.shared) {
     if (workspace == nullptr || !aligned(workspace, 256)) return DSA_ERR_INVALID_ARGUMENT;
-    if (ws_bytes < decode_partials_bytes(B, H, p.splits)) return DSA_ERR_WORKSPACE_TOO_SMALL;
-    if (B > 65535) return DSA_ERR_UNSUPPORTED;  // the merge's grid
-    p.part_o = static_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                         align256(static_cast<size_t>(B) * p.splits * H * kValueDim * 4));
+    if (ws_bytes < dsa_window_mla_workspace_size(B, H, window, sinks, latent->max_seqlen)) return DSA_ERR_WORKSPACE_TOO_SMALL;
+    // workspace: [plan][partial outputs][their maxima and sums]
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.plan = reinterpret_cast<int64_t*>(ws);
+    p.part_o = reinterpret_cast<float*>(ws + window_plan_bytes(B));
+    p.part_ml = reinterpret_cast<float*>(ws + window_plan_bytes(B) + window_part_bytes(H));
   }
   p.block_table = latent->block_table;
   p.context_lens = latent->context_lens;
-  p.max_blocks_per_seq = latent->max_blocks_per_seq;
+  p.max_blocks = latent->max_blocks_per_seq;
   p.num_blocks = latent->num_blocks;
   p.max_len = latent->max_seqlen;
   p.rows = B;
   cudaStream_t s = as_stream(stream);
-  st = launch_mla_pair<true, kMlaWindow>(latent->data, q, B, p, static_cast<int64_t>(B) * p.splits, s);
-  if (st != DSA_OK || p.splits == 1) return st;
-  mla_combine_kernel<true><<<dim3(H, B), 128, 0, s>>>(p.part_o, p.part_ml, p.splits, H, p.out, lse);
+  const dsa_status launched = launch_window<true>(latent->data, q, p, p.shared ? kMlaClusters : B, s);
+  if (launched != DSA_OK || !p.shared) return launched;
+  window_merge_kernel<<<dim3((H + 7) / 8, B), 256, 0, s>>>(p.part_o, p.part_ml, p.plan, B, H, p.out, lse);
   return launch_status();
 }
 

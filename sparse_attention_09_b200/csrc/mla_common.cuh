@@ -27,9 +27,6 @@ struct MlaParams {
   float* lse;                 // prefill: [rows, H] natural log (nullable)
   float* part_o;              // decode: [B, splits, H, 512] unnormalised
   float* part_ml;             // decode: [B, splits, H, 2] (M in log2 units, l)
-  int32_t window;             // window form: keys s > t - window ...
-  int32_t sinks;              // ... or s < sinks are visible
-  int32_t max_len;            // window form, decode: contexts are clamped to this
 };
 
 namespace mla {
@@ -40,11 +37,6 @@ __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// Copies 16 bytes, or writes 16 zero bytes without reading src (which still names mapped memory).
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst_smem, const void* src, bool copy) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "r"(copy ? 16 : 0) : "memory");
 }
 
 // Number of 64-entry chunks up to the last valid (>= 0) index of a selection row, computed by
@@ -61,9 +53,6 @@ __device__ __forceinline__ int active_chunks(const int32_t* row, int k) {
 }  // namespace mla
 
 // Merges the per-split partial results of decode: out = sum_s 2^(M_s - M) O_s / sum_s 2^(M_s - M) l_s.
-// Splits without a valid key have l = 0 and are left out; a NaN sum is left out too, or with
-// KEEP_NAN (the window form, whose softmax is defined on every visible key) carried to out and lse.
-template <bool KEEP_NAN = false>
 __global__ void __launch_bounds__(128) mla_combine_kernel(const float* __restrict__ part_o,
                                                           const float* __restrict__ part_ml, int splits, int H,
                                                           __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
@@ -71,13 +60,13 @@ __global__ void __launch_bounds__(128) mla_combine_kernel(const float* __restric
   float Mmax = -INFINITY;
   for (int s = 0; s < splits; ++s) {
     const float* ml = part_ml + ((static_cast<int64_t>(b) * splits + s) * H + h) * 2;
-    if (ml[1] > 0.f || (KEEP_NAN && ml[1] != 0.f)) Mmax = fmaxf(Mmax, ml[0]);
+    if (ml[1] > 0.f) Mmax = fmaxf(Mmax, ml[0]);
   }
   float wsum = 0.f;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < splits; ++s) {
     const float* ml = part_ml + ((static_cast<int64_t>(b) * splits + s) * H + h) * 2;
-    if (KEEP_NAN ? ml[1] == 0.f : !(ml[1] > 0.f)) continue;
+    if (!(ml[1] > 0.f)) continue;
     const float wgt = exp2f(ml[0] - Mmax);
     wsum += wgt * ml[1];
     const float4 o = *reinterpret_cast<const float4*>(part_o + ((static_cast<int64_t>(b) * splits + s) * H + h) * 512 +
@@ -87,13 +76,12 @@ __global__ void __launch_bounds__(128) mla_combine_kernel(const float* __restric
     acc[2] += wgt * o.z;
     acc[3] += wgt * o.w;
   }
-  const bool any = wsum > 0.f || (KEEP_NAN && wsum != 0.f);
-  const float inv = any ? 1.f / wsum : 0.f;
+  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
   __nv_bfloat16* orow = out + (static_cast<int64_t>(b) * H + h) * 512 + 4 * threadIdx.x;
   const uint32_t lo = dev::pack_bf16x2(acc[0] * inv, acc[1] * inv), hi = dev::pack_bf16x2(acc[2] * inv, acc[3] * inv);
   *reinterpret_cast<uint2*>(orow) = make_uint2(lo, hi);
   if (lse != nullptr && threadIdx.x == 0)
-    lse[static_cast<int64_t>(b) * H + h] = any ? (Mmax + log2f(wsum)) * 0.69314718055994531f : -INFINITY;
+    lse[static_cast<int64_t>(b) * H + h] = wsum > 0.f ? (Mmax + log2f(wsum)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace dsa

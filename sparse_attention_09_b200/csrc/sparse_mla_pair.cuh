@@ -53,7 +53,7 @@
 // workspace that a small kernel merges by log-sum-exp; an unsplit one is written as out / lse
 // directly, as in prefill.
 //
-// And the masked dense mode for short prefill (kMlaMasked): the attention a dense MHA kernel gives
+// And the masked dense mode for short prefill (MASKED): the attention a dense MHA kernel gives
 // under a mask that simulates the sparse pattern ("DeepSeek-V3.2 论文解读", section 二,
 // subsection "等性能验证").  Chunk c of token t is then the 64 contiguous latent rows
 // [64c, 64c + 64) of its sequence, for every c up to t / 64, and the keys that the (ascending)
@@ -61,15 +61,6 @@
 // read no selection entries; each softmax warp walks the selection row with a cursor (the
 // entries of chunk c are one run of at most 64 starting where chunk c - 1's run ended) and
 // loads the next run while it works on the current chunk.
-//
-// And the window form (kMlaWindow, dsa_window_mla_*): the query at position t sees its window (t - window, t]
-// and the first `sinks` tokens.  Its entries are numbered without gaps, e < ns -> position e and
-// e >= ns -> position e + (lo - ns), with lo = max(0, t + 1 - window) and ns = min(sinks, lo), so no
-// selection is read, every chunk but the last is full, and a row outside the window is never
-// loaded (a NaN there cannot reach the product P.V as 0 * NaN): entries past the last one are
-// written as zeros.  Decode splits the entries' chunks evenly; a split without a chunk runs one that
-// is masked whole.  The row sum is that of the unrounded fp32 probabilities (the lse is an fp32
-// result of its own), where the other forms sum the bf16 probabilities that the product uses.
 #pragma once
 
 #include "common.cuh"
@@ -77,9 +68,6 @@
 #include "sm100.cuh"
 
 namespace dsa {
-// How a work item's entries are found (the third template argument below).
-enum MlaForm { kMlaSparse = 0, kMlaMasked = 1, kMlaWindow = 2 };
-
 namespace mlap {
 
 constexpr int kChunk = 64;                          // selected rows per pipeline step
@@ -126,11 +114,10 @@ __device__ __forceinline__ bool pair_any(int w, bool v) {
 struct Unit {
   int64_t qrow;
   int seq, seq_start, seq_len, sp, c0, c1;
-  int ns, shift, end;  // window form: entry e < end is position e (e < ns) or e + shift
 };
 
 // Warp-collective (scans the selection row).  Masked mode: every causal chunk of the token.
-template <bool DECODE, int FORM>
+template <bool DECODE, bool MASKED>
 __device__ __forceinline__ Unit unit_of(const MlaParams& p, int64_t u) {
   Unit r;
   int kbeg, kend;
@@ -142,7 +129,7 @@ __device__ __forceinline__ Unit unit_of(const MlaParams& p, int64_t u) {
     kbeg = r.sp * per;
     kend = kbeg + per;
     r.seq_start = 0;
-    r.seq_len = min(p.context_lens[r.seq], FORM == kMlaWindow ? p.max_len : p.max_blocks_per_seq * 64);
+    r.seq_len = min(p.context_lens[r.seq], p.max_blocks_per_seq * 64);
   } else {
     r.qrow = u;
     r.sp = 0;
@@ -159,24 +146,9 @@ __device__ __forceinline__ Unit unit_of(const MlaParams& p, int64_t u) {
     r.seq_start = p.cu_seqlens[lo];
     r.seq_len = p.cu_seqlens[lo + 1] - r.seq_start;
   }
-  if constexpr (FORM == kMlaMasked) {
+  if constexpr (MASKED) {
     r.c0 = 0;
     r.c1 = static_cast<int>(u + p.unit0 - r.seq_start) / kChunk + 1;
-    return r;
-  }
-  if constexpr (FORM == kMlaWindow) {
-    const int len = max(0, DECODE ? r.seq_len : static_cast<int>(u + 1 - r.seq_start));  // keys up to the query's own
-    const int lo = max(0, len - p.window);
-    r.ns = min(p.sinks, lo);
-    r.shift = lo - r.ns;
-    r.end = len - r.shift;
-    const int64_t chunks = (static_cast<int64_t>(r.end) + kChunk - 1) / kChunk;
-    r.c0 = static_cast<int>(r.sp * chunks / p.splits);
-    r.c1 = static_cast<int>((r.sp + 1) * chunks / p.splits);
-    if (r.c1 <= r.c0) {  // no chunk for this unit: one that is masked whole
-      r.c1 = r.c0 + 1;
-      r.end = 0;
-    }
     return r;
   }
   const int act = mla::active_chunks(p.idx + r.qrow * p.k, p.k);
@@ -189,19 +161,11 @@ __device__ __forceinline__ Unit unit_of(const MlaParams& p, int64_t u) {
 // Whether selection entry v of a unit names a row of its sequence, and that row of the latent
 // array.  `bad` = neither the padding value -1 nor a usable position (or a block id outside the
 // pool): such entries are masked and reported.  Producers and softmax use this same predicate.
-// Window form: v is the entry's number.
-template <bool DECODE, int FORM>
+template <bool DECODE>
 __device__ __forceinline__ bool key_of(const MlaParams& p, const int32_t* bt, int v, const Unit& un, int& prow,
                                        bool& bad) {
-  bool valid;
-  if constexpr (FORM == kMlaWindow) {
-    valid = v < un.end;
-    bad = false;
-    if (v >= un.ns) v += un.shift;
-  } else {
-    valid = v >= 0 && v < un.seq_len;
-    bad = !valid && v != -1;
-  }
+  bool valid = v >= 0 && v < un.seq_len;
+  bad = !valid && v != -1;
   if constexpr (DECODE) {
     const int blk = valid ? bt[v >> 6] : 0;
     const bool blk_ok = blk >= 0 && blk < p.num_blocks;
@@ -209,10 +173,6 @@ __device__ __forceinline__ bool key_of(const MlaParams& p, const int32_t* bt, in
     valid = valid && blk_ok;
     if (valid) prow = blk * 64 + (v & 63);
   } else {
-    if constexpr (FORM == kMlaWindow) {  // only a negative cu_seqlens entry could lead before the array
-      bad = valid && un.seq_start + v < 0;
-      valid = valid && !bad;
-    }
     if (valid) prow = un.seq_start + v;
   }
   return valid;
@@ -220,13 +180,12 @@ __device__ __forceinline__ bool key_of(const MlaParams& p, const int32_t* bt, in
 
 }  // namespace mlap
 
-template <bool DECODE, int FORM = kMlaSparse>
+template <bool DECODE, bool MASKED = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
     sparse_mla_pair_kernel(const __nv_bfloat16* __restrict__ latent, const MlaParams p,
                            const __grid_constant__ CUtensorMap q_map) {
   using namespace dev;
   using namespace mlap;
-  constexpr bool MASKED = FORM == kMlaMasked, WINDOW = FORM == kMlaWindow;
   constexpr uint32_t IDESC_QK = idesc_bf16(128, kChunk, false, false);
   constexpr uint32_t IDESC_PV = idesc_bf16(128, 256, false, true);
 
@@ -252,9 +211,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const int cid = static_cast<int>(cluster_id_x()), ncl = static_cast<int>(num_clusters_x());
-  int64_t nunits = DECODE ? static_cast<int64_t>(p.B) * p.splits : p.rows;
-  // window form: rows behind the last sequence are no queries
-  if constexpr (WINDOW && !DECODE) nunits = min(nunits, static_cast<int64_t>(p.cu_seqlens[p.B]));
+  const int64_t nunits = DECODE ? static_cast<int64_t>(p.B) * p.splits : p.rows;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -290,10 +247,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
 
   if ((warp >= kFirstProducerWarp && warp < kFirstProducerWarp + kProducerWarps) || (warp >= kVWarp0 && warp < kVWarp0 + 2)) {
     const bool kqrole = warp < kVWarp0;
-    auto copy16 = [](uint32_t dst, const void* src, int kr) {
-      if constexpr (WINDOW) mla::cp_async16_or_zero(dst, src, kr >= 0);
-      else cp_async16(dst, src);
-    };
     // ================= gather producers =================
     // Own-row warps (4, 5): per chunk, this CTA's own 32 rows with all 576 dims (warp pw: rows
     // 16pw..16pw+15 of them, two warp instructions of 512 bytes per row plus the 128-byte rope
@@ -304,18 +257,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
     uint32_t g = 0;
     bool ok = true;
     for (int64_t u = cid; ok && u < nunits; u += ncl) {
-      const Unit un = unit_of<DECODE, FORM>(p, u);
+      const Unit un = unit_of<DECODE, MASKED>(p, u);
       const int32_t* row = p.idx + un.qrow * p.k;
       const int32_t* bt = DECODE ? p.block_table + static_cast<int64_t>(un.seq) * p.max_blocks_per_seq : nullptr;
       // masked entries still copy a real row (never NaN bits): the sequence's first key; in
       // decode the first row of its first block when that block id lies in the pool, else row 0
-      // (window form: -1, for zeros)
-      int pad_row = WINDOW ? -1 : un.seq_start;
-      if constexpr (DECODE && WINDOW) {
-        if (kqrole && pw == 0 && lane == 0 && rank == 0 && un.sp == 0 &&
-            (p.context_lens[un.seq] < 0 || p.context_lens[un.seq] > p.max_len))
-          record_device_error(DSA_ERR_DEVICE_CHECK);  // the context is clamped
-      } else if constexpr (DECODE) {
+      int pad_row = un.seq_start;
+      if constexpr (DECODE) {
         const int b0 = bt[0];
         pad_row = (b0 >= 0 && b0 < p.num_blocks) ? b0 * 64 : 0;
       }
@@ -330,25 +278,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
           int prow = pad_row;
           bool bad;
           const int e = c * kChunk + 32 * static_cast<int>(rank) + 16 * pw + (lane & 15);
-          key_of<DECODE, FORM>(p, bt, MASKED || WINDOW ? e : row[e], un, prow, bad);
+          key_of<DECODE>(p, bt, MASKED ? e : row[e], un, prow, bad);
           if (!MASKED && bad && lane < 16) record_device_error(DSA_ERR_DEVICE_CHECK);  // the entry is masked
           const uint32_t kq = smem_addr(sKQ + s * kKQBytes);
 #pragma unroll 4
           for (int j = 0; j < 16; ++j) {
             const int r = 16 * pw + j;
             const int kr = __shfl_sync(0xffffffffu, prow, j);
-            const __nv_bfloat16* src = latent + static_cast<int64_t>(WINDOW ? max(kr, 0) : kr) * 576 + 8 * lane;
+            const __nv_bfloat16* src = latent + static_cast<int64_t>(kr) * 576 + 8 * lane;
             const uint32_t off = r * 128 + (((lane & 7) ^ (r & 7)) << 4);
-            copy16(kq + (lane >> 3) * kKQBlockBytes + off, src, kr);
-            copy16(kq + (4 + (lane >> 3)) * kKQBlockBytes + off, src + 256, kr);
+            cp_async16(kq + (lane >> 3) * kKQBlockBytes + off, src);
+            cp_async16(kq + (4 + (lane >> 3)) * kKQBlockBytes + off, src + 256);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // rope dims 512-575: four rows per instruction
             const int j = 4 * i + (lane >> 3), ch = lane & 7;
             const int r = 16 * pw + j;
             const int kr = __shfl_sync(0xffffffffu, prow, j);
-            copy16(kq + 8 * kKQBlockBytes + r * 128 + ((ch ^ (r & 7)) << 4),
-                   latent + static_cast<int64_t>(WINDOW ? max(kr, 0) : kr) * 576 + 512 + 8 * ch, kr);
+            cp_async16(kq + 8 * kKQBlockBytes + r * 128 + ((ch ^ (r & 7)) << 4),
+                       latent + static_cast<int64_t>(kr) * 576 + 512 + 8 * ch);
           }
           cp_async_commit();
           cp_async_mbar_arrive(&bar_kq_full[s]);
@@ -362,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
           int prow = pad_row;
           bool bad;
           const int e = c * kChunk + 32 * pw + lane;
-          key_of<DECODE, FORM>(p, bt, MASKED || WINDOW ? e : row[e], un, prow, bad);
+          key_of<DECODE>(p, bt, MASKED ? e : row[e], un, prow, bad);
           const uint32_t vb = smem_addr(sV + s * kVBytes);
           const int seg = lane >> 4, pc = lane & 15;  // segment m: dims 256m + 128 rank + 8 pc
           const int blk = 2 * seg + (pc >> 3), ch = pc & 7;
@@ -370,9 +318,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
           for (int j = 0; j < 32; ++j) {
             const int n = 32 * pw + j;
             const int kr = __shfl_sync(0xffffffffu, prow, j);
-            copy16(vb + blk * kVBlockBytes + n * 128 + ((ch ^ (n & 7)) << 4),
-                   latent + static_cast<int64_t>(WINDOW ? max(kr, 0) : kr) * 576 + 256 * seg +
-                       128 * static_cast<int>(rank) + 8 * pc, kr);
+            cp_async16(vb + blk * kVBlockBytes + n * 128 + ((ch ^ (n & 7)) << 4),
+                       latent + static_cast<int64_t>(kr) * 576 + 256 * seg + 128 * static_cast<int>(rank) + 8 * pc);
           }
           cp_async_commit();
           cp_async_mbar_arrive(&bar_v_full[s]);
@@ -414,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
     auto enter_unit = [&](Cursor& cu) {
       cu.valid = cu.u < nunits;
       if (!cu.valid) return;
-      const Unit un = unit_of<DECODE, FORM>(p, cu.u);
+      const Unit un = unit_of<DECODE, MASKED>(p, cu.u);
       cu.c0 = un.c0;
       cu.c1 = un.c1;
       cu.c = cu.c0;
@@ -604,7 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
     uint32_t g = 0;
     bool aborted = false;
     for (int64_t u = cid; !aborted && u < nunits; u += ncl) {
-      const Unit un = unit_of<DECODE, FORM>(p, u);
+      const Unit un = unit_of<DECODE, MASKED>(p, u);
       const int32_t* row = p.idx + un.qrow * p.k;
       const int32_t* bt = DECODE ? p.block_table + static_cast<int64_t>(un.seq) * p.max_blocks_per_seq : nullptr;
       float m = -INFINITY, l = 0.f;
@@ -635,8 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
         } else {
           int prow_unused = 0;
           bool bad_unused;
-          const int e = c * kChunk + 32 * kh + lane;
-          const bool valid = key_of<DECODE, FORM>(p, bt, WINDOW ? e : row[e], un, prow_unused, bad_unused);
+          const bool valid = key_of<DECODE>(p, bt, row[c * kChunk + 32 * kh + lane], un, prow_unused, bad_unused);
           vmask = __ballot_sync(0xffffffffu, valid);
         }
         if (!pair_wait(&bar_s_full[s], (g >> 1) & 1u)) {
@@ -700,12 +646,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
           a = ((vmask >> (2 * i)) & 1u) ? a : 0.f;
           b = ((vmask >> (2 * i + 1)) & 1u) ? b : 0.f;
           pk[i] = pack_bf16x2(a, b);
-          if constexpr (WINDOW) {
-            l += a + b;
-          } else {
-            const float2 r = unpack_bf16x2(pk[i]);  // the row sum of the P that the tensor cores use
-            l += r.x + r.y;
-          }
+          const float2 r = unpack_bf16x2(pk[i]);  // the row sum of the P that the tensor cores use
+          l += r.x + r.y;
         }
         // P slot s is free once P.V of chunk g-2 has completed
         if (!pair_wait(&bar_pv_done[s], ((g >> 1) & 1u) ^ 1u)) {
@@ -734,8 +676,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
       }
       tc_fence_after();
       if (!DECODE || p.splits == 1) {  // whole selection in this unit: O / l straight to out
-        const bool any = lt > 0.f || (WINDOW && lt != 0.f);  // window form: a NaN sum stays a NaN
-        const float inv_l = any ? 1.f / lt : 0.f;
+        const float inv_l = lt > 0.f ? 1.f / lt : 0.f;
         __nv_bfloat16* orow = p.out + (un.qrow * p.H + h) * 512 + 128 * kh;
 #pragma unroll 1
         for (int cc = 0; cc < 256; cc += 32) {
@@ -754,7 +695,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mlap::kThreads, 1)
           }
         }
         if (kh == 0 && real && p.lse != nullptr)
-          p.lse[un.qrow * p.H + h] = any ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+          p.lse[un.qrow * p.H + h] = lt > 0.f ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
       } else {
         float* po = p.part_o + ((static_cast<int64_t>(un.seq) * p.splits + un.sp) * p.H + h) * 512 + 128 * kh;
 #pragma unroll 1

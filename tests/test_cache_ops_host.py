@@ -140,7 +140,7 @@ def window_decode(latent=paged(), **kw):
 
 
 COMMON = [(dict(q=None), INVALID), (dict(out=None), INVALID), (dict(latent=None), INVALID), (dict(B=0), INVALID), (dict(H=0), UNSUPPORTED),
-          (dict(H=129), UNSUPPORTED), (dict(window=0), INVALID), (dict(sinks=-1), INVALID), (dict(sm=-0.1), INVALID),
+          (dict(H=129), UNSUPPORTED), (dict(window=0), INVALID), (dict(sinks=-1), INVALID), (dict(sm=-0.1), INVALID), (dict(sm=0.0), INVALID),
           (dict(sm=float("nan")), INVALID), (dict(sm=float("inf")), INVALID), (dict(q=A + 8), INVALID), (dict(out=A + 8), INVALID),
           (dict(lse=A + 2), INVALID)]
 
@@ -165,17 +165,28 @@ def test_window_descriptor_refusals():
 
 
 def test_window_decode_workspace():
+    # chunks are shared out when the even share (a query counting 4 beside its own), a tenth of it and 15
+    # come to less than rounds of whole sequences over 74 clusters
     f = dsa.dsa_window_mla_workspace_size
     assert f(0, 128, 8, 0, 100) == 0 and f(4, 128, 0, 0, 100) == 0 and f(4, 128, 8, 0, 0) == 0
-    assert f(1, 128, 64, 0, 100000) == 0          # one 64-key chunk: nothing to split
-    assert f(64, 128, 100, 4, 100000) == 0        # few chunks and the sequences nearly fill the GPU
-    big = f(1, 128, 131072, 0, 131072)
-    assert big == 74 * 128 * 512 * 4 + 74 * 128 * 2 * 4   # one unit per CTA pair
-    assert f(1, 128, 2 ** 31 - 1, 2 ** 31 - 1, 131072) == big
-    d = paged(max_seqlen=640)
-    need = f(2, 128, 1000, 0, 640)
+
+    def expected(B, H, window, sinks, ctx):
+        chunks = -(-min(ctx, window + sinks) // 64)
+        share = B * (chunks + 4) // 74
+        if B > 1024 or chunks < 2 or not share + share // 10 + 15 < -(-B // 74) * (chunks + 4):
+            return 0
+        up = lambda n: -(-n // 256) * 256  # noqa: E731
+        return up((B + 2) * 8) + up(148 * H * 512 * 4) + up(148 * H * 8)
+
+    for B in (1, 2, 37, 63, 64, 73, 74, 75, 80, 148, 1024, 1025):
+        for window, sinks, ctx in ((64, 0, 10 ** 5), (100, 30, 10 ** 5), (512, 4, 10 ** 5), (4096, 0, 9000), (2 ** 31 - 1, 2 ** 31 - 1, 131072)):
+            assert f(B, 128, window, sinks, ctx) == expected(B, 128, window, sinks, ctx), (B, window)
+    assert f(1, 128, 64, 0, 100000) == 0 and f(3, 128, 2 ** 31 - 1, 0, 131072) > 0 and f(74, 128, 4096, 0, 131072) == 0
+    d = paged(max_seqlen=6400, per=100)
+    need = f(2, 128, 5000, 0, 6400)
     assert need > 0
-    assert window_decode(d, size=need - 1) == SMALL and window_decode(d, ws=None) == INVALID and window_decode(d, ws=A + 128) == INVALID
+    assert window_decode(d, window=5000, size=need - 1) == SMALL and window_decode(d, window=5000, ws=None) == INVALID
+    assert window_decode(d, window=5000, ws=A + 128) == INVALID
 
 
 def test_wrappers_refuse_tensors_they_cannot_pass_on():

@@ -127,9 +127,29 @@ def test_decode_heads(H):
     ctx = [300, 40, 1500]
     latent, table, logical = paged_cache(ctx)
     q = rnd((3, H, 576), 5, 2.0)
-    out, lse = decode_call(q, latent, table, ctx, 700, 2, H=H)
-    for b, c in enumerate(ctx):
-        check_row(f64(out[b]), f64(lse[b]), f64(q[b]), f64(logical[b]), c, 700, 2, (H, b))
+    for window in (700, 1400):  # whole sequences, shared out
+        out, lse = decode_call(q, latent, table, ctx, window, 2, H=H)
+        for b, c in enumerate(ctx):
+            check_row(f64(out[b]), f64(lse[b]), f64(q[b]), f64(logical[b]), c, window, 2, (H, window, b))
+
+
+@pytest.mark.parametrize("ctx", [[5000, 0, 1, 64, 900, 0], [1] * 40 + [9000] + [70] * 40, [1500] * 75, [20000], [2000, 1] * 75])
+def test_decode_shared_out(ctx):
+    """Ragged batches whose chunks are shared out: sequences in one cluster, over several, over all; empty ones between."""
+    H = 16
+    assert dsa.dsa_window_mla_workspace_size(len(ctx), H, 2 ** 30, 0, 9000 if max(ctx) < 9000 else max(ctx)) > 0
+    latent, table, logical = paged_cache(ctx)
+    if table.shape[1] * 64 < 9000:  # room to declare longer contexts than there are
+        table = torch.nn.functional.pad(table, (0, 141 - table.shape[1]), value=-1).contiguous()
+    q = rnd((len(ctx), H, 576), 5, 2.0)
+    for window, sinks in ((2 ** 30, 0), (1400, 70)):
+        out, lse = decode_call(q, latent, table, ctx, window, sinks, H=H, max_ctx=max(9000, max(ctx)))
+        assert dsa.dsa_device_error() == 0
+        again = decode_call(q, latent, table, ctx, window, sinks, H=H, max_ctx=max(9000, max(ctx)))
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)  # the same parts in the same order
+        for b, c in enumerate(ctx):
+            if b < 8 or b % 9 == 0 or c > 4000 or b > len(ctx) - 3:
+                check_row(f64(out[b]), f64(lse[b]), f64(q[b]), f64(logical[b]), c, window, sinks, (window, b))
 
 
 def test_decode_equals_the_last_prefill_row_and_the_sparse_path():
@@ -245,7 +265,7 @@ def test_two_streams_with_their_own_workspaces_and_a_captured_graph():
     n = torch.tensor(ctx, dtype=torch.int32, device="cuda")
     desc = dsa.paged_desc(latent, table, n, 3000)
     size = dsa.dsa_window_mla_workspace_size(2, 128, 1500, 4, 3000)
-    assert size > 0
+    assert size > 0  # split
     out = [torch.empty((2, 128, 512), dtype=torch.bfloat16, device="cuda") for _ in qs]
     ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in qs]
     streams = [torch.cuda.Stream() for _ in qs]
@@ -268,13 +288,13 @@ def test_two_streams_with_their_own_workspaces_and_a_captured_graph():
     assert dsa.dsa_device_error() == 0
 
 
-def test_zero_scale_is_the_mean():
+def test_vanishing_scale_gives_the_mean():
     latent, table, logical = paged_cache([100])
     q = rnd((1, 128, 576), 5)
     out, lse = torch.empty((1, 128, 512), dtype=torch.bfloat16, device="cuda"), torch.empty((1, 128), device="cuda")
     n = torch.tensor([100], dtype=torch.int32, device="cuda")
     ws = torch.empty(max(1, dsa.dsa_window_mla_workspace_size(1, 128, 10, 2, 100)), dtype=torch.uint8, device="cuda")
-    dsa.dsa_window_mla_decode(q, dsa.paged_desc(latent, table, n, 100), 1, 128, 10, 2, 0.0, out, lse, ws)
+    dsa.dsa_window_mla_decode(q, dsa.paged_desc(latent, table, n, 100), 1, 128, 10, 2, 2.0 ** -60, out, lse, ws)
     rows = f64(logical[0])[list(range(2)) + list(range(90, 100))]
     assert np.abs(f64(out[0]) - rows[:, :512].mean(0)).max() <= 2.0 ** -7 * np.abs(rows).max()
     assert np.abs(f64(lse) - math.log(12)).max() <= 2.0 ** -20
@@ -290,7 +310,7 @@ def test_wrapper_refusals():
         with pytest.raises(ValueError):
             dsa.dsa_window_mla_decode(*a[:4], 10, 0, SM, a[4])
     with pytest.raises(dsa.DSAError):
-        dsa.dsa_window_mla_decode(q, desc, 1, 128, 100, 0, SM, out)  # split, no workspace
+        dsa.dsa_window_mla_decode(q, desc, 1, 128, 100, 0, 0.0, out)
     with pytest.raises(dsa.DSAError):
         dsa.dsa_window_mla_prefill(q, desc, 1, 128, 10, 0, SM, out)  # paged
     flat = dsa.contiguous_desc(latent.flatten(0, 1), torch.tensor([0, 64], dtype=torch.int32, device="cuda"), 64)
