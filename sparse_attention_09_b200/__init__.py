@@ -380,6 +380,11 @@ def dsa_row_partition(L, k, parts, indexer_cost, mla_cost):
 _DTYPES = {torch.bfloat16: DSA_BF16, torch.float16: DSA_F16, torch.float32: DSA_F32}
 
 
+def _handle(stream, dev):
+    """The address of the stream to use: the given one or the current one of device dev."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
 def _refuse(where, name, t, dtype, shape, dense):
     return ValueError(f"{where}: {name} must be a {dtype} tensor of shape {tuple(shape)}, {dense}, on the current device, "
                       f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
@@ -407,8 +412,8 @@ def _strided(where, name, t, dtype, shape, dev):
 
 def _device(where, t):
     """The current device, for a call whose first tensor is t: all of a call's tensors are on it."""
-    dev = torch.cuda.current_device() if t.is_cuda else -1
-    if dev != t.get_device() or dev < 0:
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"{where}: tensors must be on the current CUDA device, got {t.device}")
     return dev
 
@@ -429,7 +434,8 @@ def dsa_rmsnorm(x, weight, eps, y=None, residual=None, residual_out=None, codes=
     type (bf16, fp16, fp32), any row stride; y and residual_out may be x or residual."""
     w = "dsa_rmsnorm"
     dtype, dev = _on_device(w, x, 2)
-    rows, cols = shape = tuple(x.shape)
+    shape = x.shape
+    rows, cols = shape
     xp, xl = _strided(w, "x", x, x.dtype, shape, dev)
     rp, rl = _strided(w, "residual", residual, x.dtype, shape, dev)
     yp, yl = _strided(w, "y", y, x.dtype, shape, dev)
@@ -440,7 +446,7 @@ def dsa_rmsnorm(x, weight, eps, y=None, residual=None, residual_out=None, codes=
                             yl, op, ol, _dense(w, "codes", codes, torch.uint8, shape, dev),
                             _dense(w, "scale", scale, torch.float32, (rows, groups) if grouped else (rows,), dev),
                             DSA_QUANT_GROUP if grouped else 0, _dense(w, "rstd", rstd, torch.float32, (rows,), dev),
-                            _stream(stream)), w)
+                            _handle(stream, dev)), w)
     return y if y is not None else codes
 
 
@@ -454,7 +460,8 @@ def dsa_rmsnorm_backward(dy, h, weight, rstd, dh, dw, workspace, dresidual=None,
     workspace is a uint8 tensor of dsa_rmsnorm_backward_workspace_size bytes."""
     w = "dsa_rmsnorm_backward"
     dtype, dev = _on_device(w, dy, 2)
-    rows, cols = shape = tuple(dy.shape)
+    shape = dy.shape
+    rows, cols = shape
     gp, gl = _strided(w, "dy", dy, dy.dtype, shape, dev)
     hp, hl = _strided(w, "h", h, dy.dtype, shape, dev)
     rp, rl = _strided(w, "dresidual", dresidual, dy.dtype, shape, dev)
@@ -464,7 +471,7 @@ def dsa_rmsnorm_backward(dy, h, weight, rstd, dh, dw, workspace, dresidual=None,
                                      _dense(w, "rstd", rstd, torch.float32, (rows,), dev), rp, rl, rows, cols, dtype, op, ol,
                                      _dense(w, "dw", dw, torch.float32, (cols,), dev),
                                      _dense(w, "workspace", workspace, workspace.dtype, workspace.shape, dev), size,
-                                     _stream(stream)), w)
+                                     _handle(stream, dev)), w)
     return dh, dw
 
 
@@ -475,13 +482,14 @@ def dsa_rope(x, positions, freqs, out, rot_offset, rot_dim, layout=DSA_ROPE_INTE
     its shape (the other dims are then copied).  transpose gives the backward pass."""
     w = "dsa_rope"
     dtype, dev = _on_device(w, x, 3)
-    rows, heads, dim = shape = tuple(x.shape)
+    shape = x.shape
+    rows, heads, dim = shape
     xp, xl = _strided(w, "x", x, x.dtype, shape, dev)
     op, ol = _strided(w, "out", out, x.dtype, shape, dev)
     _check(_lib.dsa_rope(xp, xl, x.stride(1), op, ol, out.stride(1), rows, heads, dim, int(rot_offset), int(rot_dim),
                          int(layout), dtype, _dense(w, "positions", positions, torch.int32, (rows,), dev),
                          _dense(w, "freqs", freqs, torch.float64, (int(rot_dim) // 2,), dev), float(mscale), int(bool(transpose)),
-                         _stream(stream)), w)
+                         _handle(stream, dev)), w)
     return out
 
 
@@ -522,7 +530,7 @@ def dsa_cache_append(kv, kv_weight, eps, key, seq, positions, freqs, latent: Des
                                  _dense(w, "positions", positions, torch.int32, (rows,), dev), rows, batch,
                                  _dense(w, "freqs", freqs, torch.float64, (32,), dev), float(mscale), int(layout),
                                  int(key_layout), int(key_rot_offset), None if latent is None else latent.ref(),
-                                 None if keys is None else keys.ref(), _stream(stream)), w)
+                                 None if keys is None else keys.ref(), _handle(stream, dev)), w)
 
 
 def _window_args(w, q, latent, B, H, out, lse):
@@ -534,18 +542,18 @@ def _window_args(w, q, latent, B, H, out, lse):
     if latent.batch != B:
         raise ValueError(f"{w}: latent describes {latent.batch} sequences, B = {B}")
     return (_dense(w, "q", q, torch.bfloat16, (rows, H, 576), dev), _dense(w, "out", out, torch.bfloat16, (rows, H, 512), dev),
-            _dense(w, "lse", lse, torch.float32, (rows, H), dev))
+            _dense(w, "lse", lse, torch.float32, (rows, H), dev), dev)
 
 
 def dsa_window_mla_prefill(q, latent: Desc, B, H, window, sinks, sm_scale, out, lse=None, stream=None):
     """MLA attention of packed prefill tokens over their last `window` keys and the first `sinks`
     tokens of their sequence (dense causal attention when window covers the sequence)."""
     w = "dsa_window_mla_prefill"
-    qp, op, lp = _window_args(w, q, latent, int(B), int(H), out, lse)
+    qp, op, lp, dev = _window_args(w, q, latent, int(B), int(H), out, lse)
     if latent.struct.kind == DSA_KV_CONTIGUOUS and q.shape[0] != latent.struct.total_tokens:
         raise ValueError(f"{w}: q has {q.shape[0]} rows, latent {latent.struct.total_tokens} tokens")
     _check(_lib.dsa_window_mla_prefill(qp, latent.ref(), int(B), int(H), int(window), int(sinks), float(sm_scale), op, lp,
-                                       _stream(stream)), w)
+                                       _handle(stream, dev)), w)
     return out
 
 
@@ -557,11 +565,11 @@ def dsa_window_mla_decode(q, latent: Desc, B, H, window, sinks, sm_scale, out, l
     """The same for one query per sequence at position ctx - 1 over the paged latent cache;
     workspace: dsa_window_mla_workspace_size bytes (None where that is 0)."""
     w = "dsa_window_mla_decode"
-    qp, op, lp = _window_args(w, q, latent, int(B), int(H), out, lse)
+    qp, op, lp, dev = _window_args(w, q, latent, int(B), int(H), out, lse)
     if q.shape[0] != B:
         raise ValueError(f"{w}: q has {q.shape[0]} rows, B = {B}")
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    wp = None if workspace is None else _dense(w, "workspace", workspace, workspace.dtype, workspace.shape, q.get_device())
+    wp = None if workspace is None else _dense(w, "workspace", workspace, workspace.dtype, workspace.shape, dev)
     _check(_lib.dsa_window_mla_decode(qp, latent.ref(), int(B), int(H), int(window), int(sinks), float(sm_scale), op, lp, wp,
-                                      size, _stream(stream)), w)
+                                      size, _handle(stream, dev)), w)
     return out
