@@ -401,9 +401,10 @@ typedef enum { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_NTK = 2, DSA_RO
  *     scale [rows, ceil(cols / 128)]), taken from the unrounded v, saturating at +-448.  NaN takes
  *     no part in the maximum and encodes as NaN.  codes and scale come together (both or neither).
  *   rstd[r] = rs                   (when not NULL; dsa_rmsnorm_backward reads it)
- * x, residual, y and residual_out are [rows, cols] of `dtype` with row strides ld_* in elements
- * (>= cols); weight [cols] of `dtype`; codes dense.  At least one of y and codes.  y or residual_out
- * may be x or residual itself (same pointer and stride); no other overlap.  Any cols >= 1 and any
+ * x, residual, y and residual_out are [rows, cols] of `dtype` with row strides ld_* in elements (of
+ * outputs >= cols; of inputs >= 0, so that rows may repeat); weight [cols] of `dtype`; codes dense.
+ * At least one of y and codes.  y or residual_out may be x or residual itself (same pointer and
+ * stride); no other overlap.  Any cols >= 1 and any
  * element-aligned pointers and strides (16-byte aligned pointers with strides and cols that are
  * multiples of 8 take the wide-load path).  rows == 0 is a no-op.
  * DSA_ERR_INVALID_ARGUMENT: NULL or misaligned pointers, sizes or strides as above, group not 0 or
@@ -421,7 +422,8 @@ dsa_status dsa_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_
  * h is the sum that was normalised (residual_out, or x without a residual), dresidual the gradient
  * that reaches residual_out; dh is the gradient of x and of residual alike.  All [rows, cols] of
  * `dtype` with row strides; weight [cols] of `dtype`, rstd [rows] and dw [cols] fp32.  Sums in fp32;
- * dw is summed in a fixed order (a run repeats its bits).  dh may be dy or dresidual itself.
+ * dw is summed in a fixed order (a run repeats its bits).  dh may be dy or dresidual itself
+ * (same pointer and stride).
  * workspace (device, 16-byte aligned): dsa_rmsnorm_backward_workspace_size(rows, cols) bytes, else
  * DSA_ERR_WORKSPACE_TOO_SMALL.  rows == 0 sets dw to zero.  Other errors as dsa_rmsnorm.
  */
@@ -437,12 +439,12 @@ size_t dsa_rmsnorm_backward_workspace_size(int64_t rows, int32_t cols);
  * angle = positions[r] * freqs[i] (radians, formed in fp64), c = mscale * cos, s = mscale * sin:
  *   (a, b) -> (a c - b s, a s + b c);   transpose != 0: (a c + b s, b c - a s), the backward pass.
  * The other dims are copied when out != x and left alone when out == x (same strides).  x and out
- * are [rows, heads, dim] of `dtype` with row and head strides in elements (head stride >= dim;
- * the row stride of one head at least dim); out either is x or overlaps it nowhere, and no two
- * (row, head) pieces of out overlap.  positions [rows] int32 (any sign), freqs [rot_dim/2] fp64 on
+ * are [rows, heads, dim] of `dtype` with row and head strides in elements (of x >= 0: a head or row
+ * may repeat when out is not x); out either is x or overlaps it nowhere, and its (row, head) pieces
+ * lie apart: each row's heads in one stretch, or each head's rows.  positions [rows] int32 (any sign), freqs [rot_dim/2] fp64 on
  * the device.  Computed in fp32, rounded once.
  * rows == 0 or heads == 0 is a no-op.  DSA_ERR_INVALID_ARGUMENT: NULL or misaligned pointers,
- * rot_dim odd or < 2, a range outside the head, strides too small, unknown layout or dtype, mscale
+ * rot_dim odd or < 2, a range outside the head, strides as above, unknown layout or dtype, mscale
  * not finite, out == x with other strides; DSA_ERR_UNSUPPORTED: rot_dim > 1024, or rows or
  * heads * dim above 2^31 - 1.
  */

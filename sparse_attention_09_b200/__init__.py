@@ -181,6 +181,7 @@ class Desc:
         self.struct = struct
         self._refs = refs
         self.batch = int(batch)  # sequences
+        self._checked = None     # (data type, row width, device) its tensors were last checked for
 
     def ref(self):
         return ctypes.byref(self.struct)
@@ -418,6 +419,23 @@ def _device(where, t):
     return dev
 
 
+def _cache(where, name, desc, dtype, width, dev):
+    """Checks the tensors of a descriptor once for this row type, width and device."""
+    if desc._checked == (dtype, width, dev):
+        return
+    data, scale, *tables = desc._refs
+    if data.dtype is not dtype or data.shape[-1] != width:
+        raise ValueError(f"{where}: {name} must describe {dtype} rows of {width}, got {data.dtype} {tuple(data.shape)}")
+    if scale is not None and (scale.dtype is not torch.float32 or scale.shape != data.shape[:-1]):
+        raise ValueError(f"{where}: {name} must have one fp32 scale per row, got {scale.dtype} {tuple(scale.shape)}")
+    for t in (data, scale, *tables):
+        if t is not None and (not t.is_contiguous() or t.get_device() != dev):
+            raise ValueError(f"{where}: the tensors that {name} describes must be contiguous, on the current device")
+    if any(t.dtype is not torch.int32 for t in tables):
+        raise ValueError(f"{where}: the tables and lengths that {name} describes must be int32")
+    desc._checked = (dtype, width, dev)
+
+
 def _on_device(where, t, dims):
     """(type code, current device) for a floating tensor of this many dimensions."""
     dev = _device(where, t)
@@ -518,10 +536,10 @@ def dsa_cache_append(kv, kv_weight, eps, key, seq, positions, freqs, latent: Des
     if key is not None:
         d_I = key.shape[-1]
         kp, kl = _strided(w, "key", key, torch.bfloat16, (rows, d_I), dev)
-    for name, desc, kind, width in (("latent", latent, torch.bfloat16, 576), ("keys", keys, torch.uint8, d_I)):
-        if desc is not None and (desc._refs[0].dtype is not kind or desc._refs[0].shape[-1] != width
-                                 or not desc._refs[0].is_contiguous() or desc._refs[0].get_device() != dev):
-            raise ValueError(f"{w}: {name} must describe a contiguous {kind} cache with rows of {width} on the current device")
+    if latent is not None:
+        _cache(w, "latent", latent, torch.bfloat16, 576, dev)
+    if keys is not None:
+        _cache(w, "keys", keys, torch.uint8, d_I, dev)
     if latent is not None and keys is not None and latent.batch != keys.batch:
         raise ValueError(f"{w}: latent describes {latent.batch} sequences, keys {keys.batch}")
     batch = latent.batch if latent is not None else keys.batch if keys is not None else 0
@@ -536,9 +554,7 @@ def dsa_cache_append(kv, kv_weight, eps, key, seq, positions, freqs, latent: Des
 def _window_args(w, q, latent, B, H, out, lse):
     rows = q.shape[0]
     dev = _device(w, q)
-    data = latent._refs[0]
-    if data.dtype is not torch.bfloat16 or data.shape[-1] != 576 or not data.is_contiguous() or data.get_device() != dev:
-        raise ValueError(f"{w}: latent must describe contiguous bf16 rows of 576 on the current device")
+    _cache(w, "latent", latent, torch.bfloat16, 576, dev)
     if latent.batch != B:
         raise ValueError(f"{w}: latent describes {latent.batch} sequences, B = {B}")
     return (_dense(w, "q", q, torch.bfloat16, (rows, H, 576), dev), _dense(w, "out", out, torch.bfloat16, (rows, H, 512), dev),

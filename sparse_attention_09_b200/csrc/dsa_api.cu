@@ -297,6 +297,11 @@ dsa_status with_dtype(int32_t dtype, F f) {
 // Whether a [rows, cols] operand (null: absent) can be read in aligned pieces of 8 elements.
 bool wide(const void* p, int64_t ld) { return p == nullptr || (aligned(p, 16) && ld % 8 == 0); }
 
+// An output that is an input itself has its row stride too.
+bool same_rows(const void* out, int64_t ld_out, const void* in, int64_t ld_in) {
+  return out == nullptr || out != in || ld_out == ld_in;
+}
+
 // Threads for a CTA-wide row of n pieces, ch per thread.
 int row_threads(int n, int ch) { return ((n + ch - 1) / ch + 31) / 32 * 32; }
 
@@ -428,7 +433,8 @@ dsa_status launch_rope(RopeParams p, bool vector, cudaStream_t s) {
 
 // One cache of dsa_cache_append from its descriptor.
 dsa_status append_cache(const dsa_kv_desc* d, bool with_scale, size_t align, AppendCache* c) {
-  if (d->data == nullptr || !aligned(d->data, align) || (with_scale && d->scale == nullptr) || d->max_seqlen <= 0)
+  if (d->data == nullptr || !aligned(d->data, align) || (with_scale && (d->scale == nullptr || !aligned(d->scale, 4))) ||
+      d->max_seqlen <= 0)
     return DSA_ERR_INVALID_ARGUMENT;
   c->data = const_cast<void*>(d->data);
   c->scale = const_cast<float*>(d->scale);
@@ -999,9 +1005,14 @@ dsa_status dsa_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_
   if (!aligned(x, es) || !aligned(residual, es) || !aligned(weight, es) || !aligned(y, es) || !aligned(residual_out, es) ||
       !aligned(scale, 4) || !aligned(rstd, 4))
     return DSA_ERR_INVALID_ARGUMENT;
-  if (ld_x < cols || (residual != nullptr && ld_residual < cols) || (y != nullptr && ld_y < cols) ||
+  if (ld_x < 0 || (residual != nullptr && ld_residual < 0) || (y != nullptr && ld_y < cols) ||
       (residual_out != nullptr && ld_residual_out < cols))
     return DSA_ERR_INVALID_ARGUMENT;
+  if (rows > 1 && (!same_rows(y, ld_y, x, ld_x) || !same_rows(y, ld_y, residual, ld_residual) ||
+                   !same_rows(residual_out, ld_residual_out, x, ld_x) ||
+                   !same_rows(residual_out, ld_residual_out, residual, ld_residual)))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (y != nullptr && y == residual_out) return DSA_ERR_INVALID_ARGUMENT;
   if (rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
   NormParams p;
   std::memset(&p, 0, sizeof(p));
@@ -1048,7 +1059,8 @@ dsa_status dsa_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, in
   if (!aligned(dy, es) || !aligned(h, es) || !aligned(weight, es) || !aligned(dresidual, es) || !aligned(dh, es) ||
       !aligned(rstd, 4) || !aligned(workspace, 16))
     return DSA_ERR_INVALID_ARGUMENT;
-  if (ld_dy < cols || ld_h < cols || ld_dh < cols || (dresidual != nullptr && ld_dresidual < cols))
+  if (ld_dy < 0 || ld_h < 0 || ld_dh < cols || (dresidual != nullptr && ld_dresidual < 0)) return DSA_ERR_INVALID_ARGUMENT;
+  if (rows > 1 && (!same_rows(dh, ld_dh, dy, ld_dy) || !same_rows(dh, ld_dh, h, ld_h) || !same_rows(dh, ld_dh, dresidual, ld_dresidual)))
     return DSA_ERR_INVALID_ARGUMENT;
   if (rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
   if (ws_bytes < dsa_rmsnorm_backward_workspace_size(rows, cols)) return DSA_ERR_WORKSPACE_TOO_SMALL;
@@ -1087,7 +1099,12 @@ dsa_status dsa_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride, 
   if (x == nullptr || out == nullptr || positions == nullptr || freqs == nullptr) return DSA_ERR_INVALID_ARGUMENT;
   const size_t es = dtype_size(dtype);
   if (!aligned(x, es) || !aligned(out, es) || !aligned(positions, 4) || !aligned(freqs, 8)) return DSA_ERR_INVALID_ARGUMENT;
-  if ((heads > 1 && (x_head_stride < dim || out_head_stride < dim)) || (rows > 1 && (x_row_stride < dim || out_row_stride < dim)))
+  if (x_row_stride < 0 || x_head_stride < 0 || out_row_stride < 0 || out_head_stride < 0) return DSA_ERR_INVALID_ARGUMENT;
+  // no two (row, head) pieces of out on one another: each row's heads in one stretch, or each head's rows
+  const int64_t head_step = heads > 1 ? out_head_stride : dim, row_step = rows > 1 ? out_row_stride : dim;
+  const int64_t far = int64_t(1) << 60;  // beyond any tensor; keeps the products in range
+  if (head_step < dim || row_step < dim || head_step > far / heads || row_step > far / rows) return DSA_ERR_INVALID_ARGUMENT;
+  if (rows > 1 && heads > 1 && row_step < head_step * (heads - 1) + dim && head_step < row_step * (rows - 1) + dim)
     return DSA_ERR_INVALID_ARGUMENT;
   if (out == x && ((rows > 1 && x_row_stride != out_row_stride) || (heads > 1 && x_head_stride != out_head_stride)))
     return DSA_ERR_INVALID_ARGUMENT;

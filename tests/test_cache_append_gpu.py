@@ -210,6 +210,11 @@ def test_wrapper_refusals():
                dict(latent=c.key_desc), dict(keys=c.lat_desc), dict(latent=other.lat_desc)):
         with pytest.raises(ValueError):
             dsa.dsa_cache_append(**{**ok, **kw})
+    wide_table = dsa.paged_desc(c.latent, c.table.long(), c.ctx, 128)
+    half_scale = dsa.paged_desc(c.codes, c.table, c.ctx, 128, scale=c.scale.half())
+    for kw in (dict(latent=wide_table), dict(keys=half_scale), dict(latent=dsa.paged_desc(c.latent, c.table.cpu(), c.ctx, 128))):
+        with pytest.raises(ValueError):
+            dsa.dsa_cache_append(**{**ok, **kw})
     for kw in (dict(kv=None), dict(keys=None), dict(key_rot_offset=66), dict(kv_weight=None), dict(layout=5)):
         with pytest.raises(dsa.DSAError):
             dsa.dsa_cache_append(**{**ok, **kw})

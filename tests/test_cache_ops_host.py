@@ -14,7 +14,7 @@ A = 4096  # an aligned address that no refused call reads
 
 
 def norm(**kw):
-    a = dict(x=A, ld_x=64, res=None, ld_res=0, w=A, rows=4, cols=64, dtype=0, eps=1e-6, y=A, ld_y=64, ro=None, ld_ro=0, codes=None,
+    a = dict(x=A, ld_x=64, res=None, ld_res=0, w=A, rows=4, cols=64, dtype=0, eps=1e-6, y=2 * A, ld_y=64, ro=None, ld_ro=0, codes=None,
              scale=None, group=0, rstd=None)
     a.update(kw)
     return dsa._lib.dsa_rmsnorm(*a.values(), None)
@@ -24,7 +24,8 @@ def norm(**kw):
     (dict(rows=0, x=None), OK), (dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(dtype=3), INVALID), (dict(dtype=-1), INVALID),
     (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID), (dict(x=None), INVALID),
     (dict(w=None), INVALID), (dict(y=None), INVALID), (dict(codes=A), INVALID), (dict(scale=A), INVALID),
-    (dict(codes=A, scale=A, group=64), INVALID), (dict(ld_x=63), INVALID), (dict(ld_y=63), INVALID), (dict(res=A, ld_res=8), INVALID),
+    (dict(codes=A, scale=A, group=64), INVALID), (dict(ld_x=-1), INVALID), (dict(y=A, x=A, ld_x=128), INVALID), (dict(y=A, res=A, ld_res=0), INVALID),
+    (dict(ro=A, ld_ro=64, y=A), INVALID), (dict(ld_y=63), INVALID), (dict(res=A, ld_res=-8), INVALID),
     (dict(ro=A, ld_ro=8), INVALID), (dict(x=A + 1), INVALID), (dict(dtype=2, x=A + 2), INVALID), (dict(codes=A, scale=A + 2), INVALID),
     (dict(rows=1 << 31), UNSUPPORTED)])
 def test_rmsnorm_refusals(kw, want):
@@ -41,8 +42,8 @@ def norm_bwd(**kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(dtype=7), INVALID), (dict(dy=None), INVALID), (dict(h=None), INVALID),
     (dict(w=None), INVALID), (dict(rstd=None), INVALID), (dict(dh=None), INVALID), (dict(dw=None), INVALID), (dict(ws=None), INVALID),
-    (dict(ws=A + 8), INVALID), (dict(ld_dy=1), INVALID), (dict(ld_h=1), INVALID), (dict(ld_dh=1), INVALID),
-    (dict(dres=A, ld_dres=3), INVALID), (dict(h=A + 1), INVALID), (dict(size=4 * 64 * 4 - 1), SMALL), (dict(rows=1 << 31), UNSUPPORTED)])
+    (dict(ws=A + 8), INVALID), (dict(ld_dy=-1), INVALID), (dict(ld_h=-1), INVALID), (dict(ld_dy=128), INVALID), (dict(ld_dh=1), INVALID),
+    (dict(dres=A, ld_dres=-3), INVALID), (dict(dh=2 * A, dres=2 * A, ld_dres=0), INVALID), (dict(h=A + 1), INVALID), (dict(size=4 * 64 * 4 - 1), SMALL), (dict(rows=1 << 31), UNSUPPORTED)])
 def test_rmsnorm_backward_refusals(kw, want):
     assert norm_bwd(**kw) == want
 
@@ -64,8 +65,8 @@ def rope(**kw):
     (dict(rows=0, x=None), OK), (dict(heads=0, x=None), OK), (dict(rows=-1), INVALID), (dict(heads=-1), INVALID), (dict(dim=0), INVALID),
     (dict(rot=63), INVALID), (dict(rot=0), INVALID), (dict(off=65), INVALID), (dict(off=-1), INVALID), (dict(rot=130), INVALID),
     (dict(layout=2), INVALID), (dict(dtype=3), INVALID), (dict(m=float("inf")), INVALID), (dict(x=None), INVALID), (dict(out=None), INVALID),
-    (dict(pos=None), INVALID), (dict(freqs=None), INVALID), (dict(freqs=A + 4), INVALID), (dict(x=A + 1), INVALID), (dict(xh=127), INVALID),
-    (dict(oh=127), INVALID), (dict(xr=100), INVALID), (dict(out=A, oh=256), INVALID), (dict(out=A, orow=1024), INVALID),
+    (dict(pos=None), INVALID), (dict(freqs=None), INVALID), (dict(freqs=A + 4), INVALID), (dict(x=A + 1), INVALID), (dict(xh=-1), INVALID),
+    (dict(oh=127), INVALID), (dict(orow=100), INVALID), (dict(orow=500), INVALID), (dict(orow=128, oh=128), INVALID), (dict(xr=-8), INVALID), (dict(out=A, oh=256), INVALID), (dict(out=A, orow=1024), INVALID),
     (dict(rows=1 << 31), UNSUPPORTED), (dict(dim=2048, xh=2048, oh=2048, xr=8192, orow=8192, rot=1026), UNSUPPORTED)])
 def test_rope_refusals(kw, want):
     assert rope(**kw) == want

@@ -140,6 +140,16 @@ def test_zero_nan_and_infinite_rows(cols, group):
     check_codes(out["codes"][rows], out["scale"][rows], v, group)
 
 
+@pytest.mark.parametrize("cols", [512, 2048, 1001])
+def test_repeated_input_rows(cols):
+    x, res, w = rnd((9, cols), torch.bfloat16, 1), rnd((1, cols), torch.bfloat16, 2).expand(9, cols), rnd((cols,), torch.bfloat16, 3)
+    want, got = forward(x, w, res.contiguous(), "row"), forward(x, w, res, "row")
+    assert all(torch.equal(got[k], want[k]) for k in ("y", "residual_out", "codes", "scale", "rstd"))
+    dres = rnd((1, cols), torch.bfloat16, 4).expand(9, cols)
+    a, b = backward(x, want["residual_out"], w, want["rstd"], dres), backward(x, want["residual_out"], w, want["rstd"], dres.contiguous())
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_zero_rows_are_no_work():
     x, w = torch.empty((0, 64), device="cuda"), torch.ones(64, device="cuda")
     dsa.dsa_rmsnorm(x, w, EPS, y=torch.empty_like(x))
@@ -271,6 +281,6 @@ def test_wrapper_refusals():
     with pytest.raises(ValueError):
         dsa.dsa_rmsnorm(x, w.half(), EPS, y=x)
     with pytest.raises(dsa.DSAError):
-        dsa.dsa_rmsnorm(x[:1].expand(4, 64), w, EPS, y=x)  # rows that overlap
+        dsa.dsa_rmsnorm(x, w, EPS, y=x[:1].expand(4, 64))  # rows of an output on one another
     with pytest.raises(dsa.DSAError):
         dsa.dsa_rmsnorm(x, w, EPS)                         # no output

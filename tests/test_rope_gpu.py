@@ -109,6 +109,18 @@ def test_strided_heads_and_rows(layout):
     check(x, pos, freqs, out, 32, 32, layout)
 
 
+@pytest.mark.parametrize("layout", [dsa.DSA_ROPE_INTERLEAVED, dsa.DSA_ROPE_HALF])
+def test_one_head_given_to_many(layout):
+    x = rnd((20, 1, 64), torch.bfloat16, 3).expand(20, 16, 64)
+    freqs, pos = dsa.dsa_rope_frequencies(64, 10000.0)[0].cuda(), torch.arange(20, dtype=torch.int32, device="cuda")
+    out, want = (torch.empty((20, 16, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dsa.dsa_rope(x, pos, freqs, out, 0, 64, layout)
+    dsa.dsa_rope(x.contiguous(), pos, freqs, want, 0, 64, layout)
+    assert torch.equal(out, want)
+    with pytest.raises(dsa.DSAError):
+        dsa.dsa_rope(x, pos, freqs, x, 0, 64, layout)  # in place on repeated heads
+
+
 def test_nothing_to_do():
     freqs = dsa.dsa_rope_frequencies(64, 10000.0)[0].cuda()
     for shape in ((0, 4, 64), (4, 0, 64)):
