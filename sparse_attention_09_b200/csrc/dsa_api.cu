@@ -245,11 +245,11 @@ dsa_status launch_mla_pair(const void* latent, const void* q, int64_t q_rows, co
 // ---- window MLA --------------------------------------------------------------------------------
 // Whether decode shares the chunks of all sequences out over the clusters (and merges the split
 // sequences) instead of giving each cluster whole sequences.  In chunks' times: whole sequences take
-// rounds of (chunks + kUnitCost); shared, the even share, 15 for what a split adds (a second piece of
-// work per cluster, fp32 partial outputs, the merge's launch) and a tenth of the share.  By the longest
-// context the arguments allow: the contexts themselves are on the device.
-// Measured (us, shared / whole): 16 sequences of 1024 keys 27.7 / 28.0, of 2048 31.8 / 46.0; of 4096 keys
-// 32 sequences 66 / 89, 64: 107 / 95, 80: 128 / 177, 128: 190 / 183; 8 of 512 21.5 / 19.4.
+// rounds of (chunks + kUnitCost); shared, the even share, a quarter of it and 12 for what splits add (a
+// second piece of work per cluster, fp32 partial outputs, the merge).  By the longest context the
+// arguments allow: the contexts themselves are on the device.
+// Measured (us, shared / whole): 8 sequences of 512 keys 20.6 / 19.6; 16 of 1024 27.5 / 27.8, of 2048
+// 31.8 / 45.9; of 4096 keys 48 sequences 82 / 85, 64: 103 / 90, 80: 125 / 163, 112: 177 / 165, 160: 235 / 247.
 constexpr int kShareSeqs = 1024;  // a cluster's start is found by a scan of the contexts
 
 bool window_shared(int B, int window, int sinks, int max_ctx) {
@@ -258,10 +258,10 @@ bool window_shared(int B, int window, int sinks, int max_ctx) {
   if (B > kShareSeqs || chunks < 2) return false;
   const int64_t whole = (B + kMlaClusters - 1) / kMlaClusters * (chunks + win::kUnitCost);
   const int64_t share = B * (chunks + win::kUnitCost) / kMlaClusters;
-  return share + share / 10 + 15 < whole;
+  return share + share / 4 + 12 < whole;
 }
 
-size_t window_plan_bytes(int B) { return align256((static_cast<size_t>(B) + 2) * sizeof(int64_t)); }
+size_t window_plan_bytes(int B) { return align256(static_cast<size_t>(B) * sizeof(int2)); }
 size_t window_part_bytes(int H) { return align256(static_cast<size_t>(2 * kMlaClusters) * H * kValueDim * 4); }
 
 template <bool DECODE>
@@ -1284,7 +1284,7 @@ dsa_status dsa_window_mla_decode(const void* q, const dsa_kv_desc* latent, int32
     if (ws_bytes < dsa_window_mla_workspace_size(B, H, window, sinks, latent->max_seqlen)) return DSA_ERR_WORKSPACE_TOO_SMALL;
     // workspace: [plan][partial outputs][their maxima and sums]
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.plan = reinterpret_cast<int64_t*>(ws);
+    p.plan = reinterpret_cast<int2*>(ws);
     p.part_o = reinterpret_cast<float*>(ws + window_plan_bytes(B));
     p.part_ml = reinterpret_cast<float*>(ws + window_plan_bytes(B) + window_part_bytes(H));
   }
@@ -1297,7 +1297,7 @@ dsa_status dsa_window_mla_decode(const void* q, const dsa_kv_desc* latent, int32
   cudaStream_t s = as_stream(stream);
   const dsa_status launched = launch_window<true>(latent->data, q, p, p.shared ? kMlaClusters : B, s);
   if (launched != DSA_OK || !p.shared) return launched;
-  window_merge_kernel<<<dim3((H + 7) / 8, B), 256, 0, s>>>(p.part_o, p.part_ml, p.plan, B, H, p.out, lse);
+  window_merge_kernel<<<dim3(H, B), 128, 0, s>>>(p.part_o, p.part_ml, p.plan, H, p.out, lse);
   return launch_status();
 }
 

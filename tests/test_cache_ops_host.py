@@ -166,7 +166,7 @@ def test_window_descriptor_refusals():
 
 
 def test_window_decode_workspace():
-    # chunks are shared out when the even share (a query counting 4 beside its own), a tenth of it and 15
+    # chunks are shared out when the even share (a query counting 4 beside its own), a quarter of it and 12
     # come to less than rounds of whole sequences over 74 clusters
     f = dsa.dsa_window_mla_workspace_size
     assert f(0, 128, 8, 0, 100) == 0 and f(4, 128, 0, 0, 100) == 0 and f(4, 128, 8, 0, 0) == 0
@@ -174,10 +174,10 @@ def test_window_decode_workspace():
     def expected(B, H, window, sinks, ctx):
         chunks = -(-min(ctx, window + sinks) // 64)
         share = B * (chunks + 4) // 74
-        if B > 1024 or chunks < 2 or not share + share // 10 + 15 < -(-B // 74) * (chunks + 4):
+        if B > 1024 or chunks < 2 or not share + share // 4 + 12 < -(-B // 74) * (chunks + 4):
             return 0
         up = lambda n: -(-n // 256) * 256  # noqa: E731
-        return up((B + 2) * 8) + up(148 * H * 512 * 4) + up(148 * H * 8)
+        return up(B * 8) + up(148 * H * 512 * 4) + up(148 * H * 8)
 
     for B in (1, 2, 37, 63, 64, 73, 74, 75, 80, 148, 1024, 1025):
         for window, sinks, ctx in ((64, 0, 10 ** 5), (100, 30, 10 ** 5), (512, 4, 10 ** 5), (4096, 0, 9000), (2 ** 31 - 1, 2 ** 31 - 1, 131072)):
