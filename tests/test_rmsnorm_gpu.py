@@ -30,8 +30,9 @@ def f64(t):
     return t.double().cpu().numpy()
 
 
-def close(got, want, mag, what, rel=F32):
-    """|got - want| <= rounding of the type + rel * mag, element by element; infinities equal."""
+def close(got, want, mag, what, rel=None):
+    """|got - want| <= rounding of the type + rel * mag, element by element."""
+    rel = rel or (F32 if got.shape[-1] <= 16384 else 2 * F32)
     half = torch.finfo(got.dtype).eps / 2
     err = np.abs(f64(got) - want)
     bound = np.abs(want) * half * (1 + 2.0 ** -10) + TINY[got.dtype] + rel * mag
@@ -41,11 +42,12 @@ def close(got, want, mag, what, rel=F32):
 
 def check_codes(codes, scale, v, group):
     want = oracle.row_scales(v, group)
-    assert np.all(np.abs(f64(scale) - want) <= want * (F32 + 2.0 ** -24)), "scales"
+    rel = F32 if v.shape[1] <= 16384 else 2 * F32
+    assert np.all(np.abs(f64(scale) - want) <= want * (rel + 2.0 ** -24)), "scales"
     s = f64(scale)
     s = np.repeat(s, group, axis=1)[:, :v.shape[1]] if group else s[:, None]
     got = oracle.decode_e4m3(codes.cpu().numpy()) * s
-    bound = np.maximum(np.abs(v) * 2.0 ** -4, s * 2.0 ** -10) * (1 + 2.0 ** -10) + np.abs(v) * F32
+    bound = np.maximum(np.abs(v) * 2.0 ** -4, s * 2.0 ** -10) * (1 + 2.0 ** -10) + np.abs(v) * rel
     assert np.all(np.abs(got - v) <= bound), "codes"
 
 
@@ -68,13 +70,13 @@ def check_forward(x, w, residual, quant, out):
     if residual is not None:
         close(out["residual_out"], h, np.abs(h), "residual_out")
     if out["rstd"] is not None:
-        close(out["rstd"], rstd, rstd, "rstd")
+        close(out["rstd"], rstd, rstd, "rstd", rel=2 * F32)
     if quant != "none":
         check_codes(out["codes"], out["scale"], v, 128 if quant == "group" else 0)
 
 
 # one lane, less than a warp, a warp's four pieces and one more, each register form, the widest, beyond it, odd
-COLS = [1, 8, 120, 128, 250, 256, 264, 512, 1000, 1001, 1024, 1032, 2048, 4096, 5120, 8192, 16384, 4103]
+COLS = [1, 8, 120, 128, 250, 256, 264, 512, 1000, 1001, 1024, 1032, 2048, 4096, 5120, 8192, 16384, 4103, 9001, 20000, 33001]
 
 
 @pytest.mark.parametrize("cols", COLS)
