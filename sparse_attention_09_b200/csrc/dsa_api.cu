@@ -356,7 +356,7 @@ dsa_status launch_rmsnorm_backward_v(const NormBwdParams& p, float* dw, cudaStre
   }
   const dsa_status st = launch_status();
   if (st != DSA_OK) return st;
-  rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 256, 0, s>>>(p.part, static_cast<int>(ctas), p.cols, dw);
+  rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 1024, 0, s>>>(p.part, static_cast<int>(ctas), p.cols, dw);
   return launch_status();
 }
 
@@ -376,7 +376,7 @@ dsa_status launch_rmsnorm_backward(const NormBwdParams& p, bool vector, float* d
       rmsnorm_backward_ring_kernel<T><<<static_cast<unsigned>(ctas), row_threads(n, 1), smem, s>>>(p, stages);
       const dsa_status st = launch_status();
       if (st != DSA_OK) return st;
-      rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 256, 0, s>>>(p.part, static_cast<int>(ctas), p.cols, dw);
+      rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 1024, 0, s>>>(p.part, static_cast<int>(ctas), p.cols, dw);
       return launch_status();
     }
     if (n <= 2 * 1024) return launch_rmsnorm_backward_v<T, 8, 2, false>(p, dw, s);
@@ -390,7 +390,7 @@ dsa_status launch_rmsnorm_backward(const NormBwdParams& p, bool vector, float* d
   rmsnorm_backward_general_kernel<T><<<static_cast<unsigned>(ctas), norm::kGeneralThreads, 0, s>>>(p);
   const dsa_status st = launch_status();
   if (st != DSA_OK) return st;
-  rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 256, 0, s>>>(p.part, static_cast<int>(ctas), p.cols, dw);
+  rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 1024, 0, s>>>(p.part, static_cast<int>(ctas), p.cols, dw);
   return launch_status();
 }
 

@@ -537,22 +537,19 @@ __global__ void __launch_bounds__(norm::kGeneralThreads) rmsnorm_backward_genera
   }
 }
 
-// dw[c] = sum of the n partial rows, in a fixed order: 32 columns per CTA, 8 threads per column.
-__global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float* __restrict__ part, int n, int cols,
-                                                         float* __restrict__ dw) {
-  __shared__ float s[8][32];
+// dw[c] = sum of the n partial rows, in a fixed order: 32 columns per CTA, 32 threads per column.
+__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* __restrict__ part, int n, int cols,
+                                                          float* __restrict__ dw) {
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float acc = 0.f;
   if (c < cols)
-    for (int i = k; i < n; i += 8) acc += part[static_cast<int64_t>(i) * cols + c];
+    for (int i = k; i < n; i += 32) acc += part[static_cast<int64_t>(i) * cols + c];
   s[k][lane] = acc;
   __syncthreads();
-  if (k == 0 && c < cols) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) acc += s[i][lane];
-    dw[c] = acc;
-  }
+  const float sum = elem::warp_sum(s[lane][k]);  // warp k: column k of the CTA
+  if (lane == 0 && blockIdx.x * 32 + k < cols) dw[blockIdx.x * 32 + k] = sum;
 }
 
 }  // namespace dsa
