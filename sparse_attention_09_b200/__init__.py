@@ -2,8 +2,9 @@
 
 Argument marshalling only: every function passes device pointers (``tensor.data_ptr()``),
 sizes and the current CUDA stream to the C ABI declared in ``include/dsa.h`` and raises
-``DSAError`` on a non-zero status.  All computation happens in the library's CUDA kernels;
-there is no fallback.  Importing fails if the library has not been built
+``DSAError`` on a non-zero status.  The calls around the caches go through a small compiled module
+(``_marshal``) that also checks their tensors and raises ``ValueError``.  All computation happens in
+the library's CUDA kernels; there is no fallback.  Importing fails if the library has not been built
 (``python sparse_attention_09_b200/build.py``).
 """
 
@@ -18,6 +19,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdsa.so"
 if not os.path.exists(_LIB_PATH):
     raise ImportError(f"libdsa.so is not built ({_LIB_PATH}); run: python sparse_attention_09_b200/build.py")
 _lib = ctypes.CDLL(_LIB_PATH)
+from . import _marshal  # noqa: E402  (after torch and the library, which it links)
 
 DSA_OK = 0
 DSA_ERR_INVALID_ARGUMENT = 1
@@ -181,6 +183,7 @@ class Desc:
         self.struct = struct
         self._refs = refs
         self.batch = int(batch)  # sequences
+        self._address = ctypes.addressof(struct)
         self._checked = None     # (data type, row width, device) its tensors were last checked for
 
     def ref(self):
@@ -374,50 +377,9 @@ def dsa_row_partition(L, k, parts, indexer_cost, mla_cost):
 
 
 # ---- operators around the caches: norm, rotary positions, cache append, window attention ----------
-# These take tensors whose type, shape and strides the C ABI cannot see, so each is checked here
-# (ValueError); a tensor on another device than the current one is refused, because the stream the
-# work goes to is the current device's.
-
-_DTYPES = {torch.bfloat16: DSA_BF16, torch.float16: DSA_F16, torch.float32: DSA_F32}
-
-
-def _handle(stream, dev):
-    """The address of the stream to use: the given one or the current one of device dev."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _refuse(where, name, t, dtype, shape, dense):
-    return ValueError(f"{where}: {name} must be a {dtype} tensor of shape {tuple(shape)}, {dense}, on the current device, "
-                      f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-
-
-def _dense(where, name, t, dtype, shape, dev):
-    """The address of a contiguous tensor of this type and shape on device dev (None: NULL)."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
-        return t.data_ptr()
-    raise _refuse(where, name, t, dtype, shape, "contiguous")
-
-
-def _strided(where, name, t, dtype, shape, dev):
-    """(address, row stride) of a tensor of this type and shape whose last dimension is dense."""
-    if t is None:
-        return None, 0
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
-        stride = t.stride()
-        if stride[-1] == 1 or shape[-1] <= 1:
-            return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], shape[-1])
-    raise _refuse(where, name, t, dtype, shape, "dense in its last dimension")
-
-
-def _device(where, t):
-    """The current device, for a call whose first tensor is t: all of a call's tensors are on it."""
-    dev = t.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
-        raise ValueError(f"{where}: tensors must be on the current CUDA device, got {t.device}")
-    return dev
-
+# Their tensors are checked (ValueError) by the compiled module, which knows types, shapes and strides;
+# a tensor on another device than the current one is refused, because the stream the work goes to is the
+# current device's.
 
 def _cache(where, name, desc, dtype, width, dev):
     """Checks the tensors of a descriptor once for this row type, width and device."""
@@ -436,13 +398,8 @@ def _cache(where, name, desc, dtype, width, dev):
     desc._checked = (dtype, width, dev)
 
 
-def _on_device(where, t, dims):
-    """(type code, current device) for a floating tensor of this many dimensions."""
-    dev = _device(where, t)
-    code = _DTYPES.get(t.dtype)
-    if code is None or t.dim() != dims:
-        raise ValueError(f"{where}: expected a bf16, fp16 or fp32 tensor of {dims} dimensions, got {t.dtype} {tuple(t.shape)}")
-    return code, dev
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def dsa_rmsnorm(x, weight, eps, y=None, residual=None, residual_out=None, codes=None, scale=None, rstd=None, stream=None):
@@ -450,21 +407,7 @@ def dsa_rmsnorm(x, weight, eps, y=None, residual=None, residual_out=None, codes=
     (uint8) with scale [rows] (one per row) or [rows, ceil(cols / 128)] (one per 128 columns);
     residual_out = h; rstd [rows] for the backward.  x, residual, y, residual_out: [rows, cols] of one
     type (bf16, fp16, fp32), any row stride; y and residual_out may be x or residual."""
-    w = "dsa_rmsnorm"
-    dtype, dev = _on_device(w, x, 2)
-    shape = x.shape
-    rows, cols = shape
-    xp, xl = _strided(w, "x", x, x.dtype, shape, dev)
-    rp, rl = _strided(w, "residual", residual, x.dtype, shape, dev)
-    yp, yl = _strided(w, "y", y, x.dtype, shape, dev)
-    op, ol = _strided(w, "residual_out", residual_out, x.dtype, shape, dev)
-    groups = -(-cols // DSA_QUANT_GROUP)
-    grouped = scale is not None and scale.dim() == 2
-    _check(_lib.dsa_rmsnorm(xp, xl, rp, rl, _dense(w, "weight", weight, x.dtype, (cols,), dev), rows, cols, dtype, float(eps), yp,
-                            yl, op, ol, _dense(w, "codes", codes, torch.uint8, shape, dev),
-                            _dense(w, "scale", scale, torch.float32, (rows, groups) if grouped else (rows,), dev),
-                            DSA_QUANT_GROUP if grouped else 0, _dense(w, "rstd", rstd, torch.float32, (rows,), dev),
-                            _handle(stream, dev)), w)
+    _check(_marshal.rmsnorm(x, weight, eps, y, residual, residual_out, codes, scale, rstd, _handle(stream)), "dsa_rmsnorm")
     return y if y is not None else codes
 
 
@@ -476,20 +419,7 @@ def dsa_rmsnorm_backward(dy, h, weight, rstd, dh, dw, workspace, dresidual=None,
     """Gradients of dsa_rmsnorm: dh [rows, cols] (of x and of residual; plus dresidual, the gradient
     of residual_out) and dw [cols] fp32 from dy, h (residual_out, or x without a residual) and rstd;
     workspace is a uint8 tensor of dsa_rmsnorm_backward_workspace_size bytes."""
-    w = "dsa_rmsnorm_backward"
-    dtype, dev = _on_device(w, dy, 2)
-    shape = dy.shape
-    rows, cols = shape
-    gp, gl = _strided(w, "dy", dy, dy.dtype, shape, dev)
-    hp, hl = _strided(w, "h", h, dy.dtype, shape, dev)
-    rp, rl = _strided(w, "dresidual", dresidual, dy.dtype, shape, dev)
-    op, ol = _strided(w, "dh", dh, dy.dtype, shape, dev)
-    size = workspace.numel() * workspace.element_size()
-    _check(_lib.dsa_rmsnorm_backward(gp, gl, hp, hl, _dense(w, "weight", weight, dy.dtype, (cols,), dev),
-                                     _dense(w, "rstd", rstd, torch.float32, (rows,), dev), rp, rl, rows, cols, dtype, op, ol,
-                                     _dense(w, "dw", dw, torch.float32, (cols,), dev),
-                                     _dense(w, "workspace", workspace, workspace.dtype, workspace.shape, dev), size,
-                                     _handle(stream, dev)), w)
+    _check(_marshal.rmsnorm_backward(dy, h, weight, rstd, dh, dw, workspace, dresidual, _handle(stream)), "dsa_rmsnorm_backward")
     return dh, dw
 
 
@@ -498,16 +428,7 @@ def dsa_rope(x, positions, freqs, out, rot_offset, rot_dim, layout=DSA_ROPE_INTE
     """Rotates dims [rot_offset, rot_offset + rot_dim) of every head of x [rows, heads, dim] by
     positions[row] * freqs (int32 [rows], float64 [rot_dim / 2]) into out, which is x itself or of
     its shape (the other dims are then copied).  transpose gives the backward pass."""
-    w = "dsa_rope"
-    dtype, dev = _on_device(w, x, 3)
-    shape = x.shape
-    rows, heads, dim = shape
-    xp, xl = _strided(w, "x", x, x.dtype, shape, dev)
-    op, ol = _strided(w, "out", out, x.dtype, shape, dev)
-    _check(_lib.dsa_rope(xp, xl, x.stride(1), op, ol, out.stride(1), rows, heads, dim, int(rot_offset), int(rot_dim),
-                         int(layout), dtype, _dense(w, "positions", positions, torch.int32, (rows,), dev),
-                         _dense(w, "freqs", freqs, torch.float64, (int(rot_dim) // 2,), dev), float(mscale), int(bool(transpose)),
-                         _handle(stream, dev)), w)
+    _check(_marshal.rope(x, positions, freqs, out, rot_offset, rot_dim, layout, mscale, transpose, _handle(stream)), "dsa_rope")
     return out
 
 
@@ -529,47 +450,31 @@ def dsa_cache_append(kv, kv_weight, eps, key, seq, positions, freqs, latent: Des
     position positions[r] of sequence seq[r] (seq None: sequence r; -1: skipped) of the caches that
     latent and keys describe.  kv, kv_weight and latent, or key and keys, may be None."""
     w = "dsa_cache_append"
-    dev = _device(w, positions)
-    rows = positions.shape[0]
-    kp, kl, d_I = None, 0, 128
-    vp, vl = _strided(w, "kv", kv, torch.bfloat16, (rows, 576), dev)
-    if key is not None:
-        d_I = key.shape[-1]
-        kp, kl = _strided(w, "key", key, torch.bfloat16, (rows, d_I), dev)
+    dev = positions.get_device()
     if latent is not None:
         _cache(w, "latent", latent, torch.bfloat16, 576, dev)
     if keys is not None:
-        _cache(w, "keys", keys, torch.uint8, d_I, dev)
-    if latent is not None and keys is not None and latent.batch != keys.batch:
-        raise ValueError(f"{w}: latent describes {latent.batch} sequences, keys {keys.batch}")
-    batch = latent.batch if latent is not None else keys.batch if keys is not None else 0
-    _check(_lib.dsa_cache_append(vp, vl, _dense(w, "kv_weight", kv_weight, torch.bfloat16, (512,), dev), float(eps), kp, kl, d_I,
-                                 _dense(w, "seq", seq, torch.int32, (rows,), dev),
-                                 _dense(w, "positions", positions, torch.int32, (rows,), dev), rows, batch,
-                                 _dense(w, "freqs", freqs, torch.float64, (32,), dev), float(mscale), int(layout),
-                                 int(key_layout), int(key_rot_offset), None if latent is None else latent.ref(),
-                                 None if keys is None else keys.ref(), _handle(stream, dev)), w)
+        _cache(w, "keys", keys, torch.uint8, 128 if key is None else key.shape[-1], dev)
+        if latent is not None and latent.batch != keys.batch:
+            raise ValueError(f"{w}: latent describes {latent.batch} sequences, keys {keys.batch}")
+    some = latent or keys
+    _check(_marshal.cache_append(kv, kv_weight, eps, key, seq, positions, freqs, latent and latent._address,
+                                 keys and keys._address, some.batch if some else 0, layout, key_layout, key_rot_offset, mscale,
+                                 _handle(stream)), w)
 
 
-def _window_args(w, q, latent, B, H, out, lse):
-    rows = q.shape[0]
-    dev = _device(w, q)
-    _cache(w, "latent", latent, torch.bfloat16, 576, dev)
+def _windowed(w, q, latent, B):
+    _cache(w, "latent", latent, torch.bfloat16, 576, q.get_device())
     if latent.batch != B:
         raise ValueError(f"{w}: latent describes {latent.batch} sequences, B = {B}")
-    return (_dense(w, "q", q, torch.bfloat16, (rows, H, 576), dev), _dense(w, "out", out, torch.bfloat16, (rows, H, 512), dev),
-            _dense(w, "lse", lse, torch.float32, (rows, H), dev), dev)
+    return latent._address
 
 
 def dsa_window_mla_prefill(q, latent: Desc, B, H, window, sinks, sm_scale, out, lse=None, stream=None):
     """MLA attention of packed prefill tokens over their last `window` keys and the first `sinks`
     tokens of their sequence (dense causal attention when window covers the sequence)."""
     w = "dsa_window_mla_prefill"
-    qp, op, lp, dev = _window_args(w, q, latent, int(B), int(H), out, lse)
-    if latent.struct.kind == DSA_KV_CONTIGUOUS and q.shape[0] != latent.struct.total_tokens:
-        raise ValueError(f"{w}: q has {q.shape[0]} rows, latent {latent.struct.total_tokens} tokens")
-    _check(_lib.dsa_window_mla_prefill(qp, latent.ref(), int(B), int(H), int(window), int(sinks), float(sm_scale), op, lp,
-                                       _handle(stream, dev)), w)
+    _check(_marshal.window_prefill(q, _windowed(w, q, latent, B), B, H, window, sinks, sm_scale, out, lse, _handle(stream)), w)
     return out
 
 
@@ -581,11 +486,6 @@ def dsa_window_mla_decode(q, latent: Desc, B, H, window, sinks, sm_scale, out, l
     """The same for one query per sequence at position ctx - 1 over the paged latent cache;
     workspace: dsa_window_mla_workspace_size bytes (None where that is 0)."""
     w = "dsa_window_mla_decode"
-    qp, op, lp, dev = _window_args(w, q, latent, int(B), int(H), out, lse)
-    if q.shape[0] != B:
-        raise ValueError(f"{w}: q has {q.shape[0]} rows, B = {B}")
-    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    wp = None if workspace is None else _dense(w, "workspace", workspace, workspace.dtype, workspace.shape, dev)
-    _check(_lib.dsa_window_mla_decode(qp, latent.ref(), int(B), int(H), int(window), int(sinks), float(sm_scale), op, lp, wp,
-                                      size, _handle(stream, dev)), w)
+    _check(_marshal.window_decode(q, _windowed(w, q, latent, B), B, H, window, sinks, sm_scale, out, lse, workspace,
+                                  _handle(stream)), w)
     return out

@@ -1,4 +1,5 @@
-"""Builds libdsa.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a.
+"""Builds libdsa.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a, and _marshal.so (the Python
+module that checks tensors and calls it) with g++.
 
 Usage: python sparse_attention_09_b200/build.py [--verbose]
 """
@@ -14,6 +15,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libdsa.so")
+MARSHAL_PATH = os.path.join(PKG_DIR, "_marshal.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -39,14 +41,45 @@ def _stale() -> bool:
     if not os.path.exists(LIB_PATH):
         return True
     t = os.path.getmtime(LIB_PATH)
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "dsa.h")]
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "marshal.cpp"] + [os.path.join(ROOT, "include", "dsa.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_marshal(force: bool) -> None:
+    """Compile _marshal.so against the libraries that torch loads (found by their names: torch is imported first)."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    deps = [src, os.path.join(ROOT, "include", "dsa.h")]
+    if not force and os.path.exists(MARSHAL_PATH) and all(os.path.getmtime(d) <= os.path.getmtime(MARSHAL_PATH) for d in deps):
+        return
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = MARSHAL_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(base, "include"), "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"), src, "-o", tmp,
+           "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-L", PKG_DIR, "-ldsa", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, cwd=ROOT, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    os.replace(tmp, MARSHAL_PATH)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if any source is newer than the built .so; returns its path."""
+    """Compile the library and the Python module if a source is newer than what is built; returns the library's path."""
+    _build_library(force, verbose)
+    _build_marshal(force)
+    return LIB_PATH
+
+
+def _build_library(force: bool, verbose: bool) -> None:
     if not force and not _stale():
-        return LIB_PATH
+        return
     tmp = LIB_PATH + ".tmp"
     cmd = [_nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), *sources(), "-o", tmp]
     if verbose:
@@ -58,7 +91,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(res.stdout + res.stderr)
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":
