@@ -394,12 +394,23 @@ dsa_status launch_rmsnorm_backward(const NormBwdParams& p, bool vector, float* d
   return launch_status();
 }
 
+// piece: elements that heads, strides and pointers divide into (8, 4, 2 or 1).
 template <typename T>
-dsa_status launch_rope(RopeParams p, bool vector, cudaStream_t s) {
+dsa_status launch_rope(RopeParams p, int piece, cudaStream_t s) {
   const int pairs = p.rot / 2;
   const int rest = p.copy_rest ? p.dim - p.rot : 0;
-  if (vector) p.items = p.rot / (p.half_layout ? 16 : 8) + rest / 8;
-  else p.items = pairs + rest;
+  // the rotated range (in the half layout each of its halves) made of whole pieces, of 8 or of 4
+  auto in_pieces = [&](int v) { return piece >= v && p.rot0 % v == 0 && (p.half_layout ? pairs : p.rot) % v == 0; };
+  const int whole = in_pieces(8) ? 8 : in_pieces(4) ? 4 : 0;
+  if (whole != 0) {
+    p.items = (p.half_layout ? pairs : p.rot) / whole + rest / whole;
+  } else if (p.copy_rest) {
+    const int from = p.rot0 / piece * piece, to = (p.rot0 + p.rot + piece - 1) / piece * piece;
+    p.items = pairs + (to - from - p.rot) + (p.dim - (to - from)) / piece;
+  } else {
+    p.items = pairs;
+    piece = 1;
+  }
   p.lanes = std::min(p.items, rope::kThreads);
   // groups per CTA: as many as fit, but a divisor of the heads when that costs less than half
   p.groups = rope::kThreads / p.lanes;
@@ -408,9 +419,10 @@ dsa_status launch_rope(RopeParams p, bool vector, cudaStream_t s) {
       p.groups = g;
       break;
     }
-  // A CTA walks one batch of (row, head) pairs: several rows when a row has fewer, a range of a row's
-  // heads when it has more (each CTA makes its own table of rot / 2 entries per row).
-  const int batch = p.groups * rope::unroll<T>();
+  // A CTA walks one batch of (row, head) pairs, or with small pieces some: several rows when a row has
+  // fewer, a range of a row's heads when it has more (each CTA makes its own table of rot / 2 entries per
+  // row).
+  const int batch = p.groups * rope::unroll<T>() * (whole == 8 ? 1 : 2);
   int64_t parts = 1;
   p.rows_per_cta = 1;
   p.heads_per_cta = p.heads;
@@ -425,9 +437,13 @@ dsa_status launch_rope(RopeParams p, bool vector, cudaStream_t s) {
   const int64_t ctas = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
   const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(parts));
   const int threads = (p.groups * p.lanes + 31) / 32 * 32;
-  if (!vector) rope_kernel<T, 1, false><<<grid, threads, 0, s>>>(p);
-  else if (p.half_layout) rope_kernel<T, 8, true><<<grid, threads, 0, s>>>(p);
-  else rope_kernel<T, 8, false><<<grid, threads, 0, s>>>(p);
+  auto launch = [&](auto kern) { kern<<<grid, threads, 0, s>>>(p); };
+  if (whole == 8) launch(p.half_layout ? rope_kernel<T, 8, true> : rope_kernel<T, 8, false>);
+  else if (whole == 4) launch(p.half_layout ? rope_kernel<T, 4, true> : rope_kernel<T, 4, false>);
+  else if (piece == 8) launch(rope_pairs_kernel<T, 8>);
+  else if (piece == 4) launch(rope_pairs_kernel<T, 4>);
+  else if (piece == 2) launch(rope_pairs_kernel<T, 2>);
+  else launch(rope_pairs_kernel<T, 1>);
   return launch_status();
 }
 
@@ -1129,14 +1145,17 @@ dsa_status dsa_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride, 
   p.mscale = mscale;
   p.transpose = transpose;
   p.copy_rest = out != x;
-  const int piece = layout == DSA_ROPE_HALF ? 16 : 8;  // both halves of a pair lie in whole pieces
-  auto strides_ok = [](int64_t row, int64_t head, int64_t r, int h) { return (r <= 1 || row % 8 == 0) && (h <= 1 || head % 8 == 0); };
-  const bool vector = dim % 8 == 0 && rot_offset % 8 == 0 && rot_dim % piece == 0 && aligned(x, 16) && aligned(out, 16) &&
-                      strides_ok(x_row_stride, x_head_stride, rows, heads) &&
-                      strides_ok(out_row_stride, out_head_stride, rows, heads);
+  int piece = 8;
+  auto divides = [&](int v) {
+    const size_t bytes = std::min<size_t>(v * es, 16);
+    auto ok = [&](int64_t stride, int64_t n) { return n <= 1 || stride % v == 0; };
+    return dim % v == 0 && aligned(x, bytes) && aligned(out, bytes) && ok(x_row_stride, rows) && ok(x_head_stride, heads) &&
+           ok(out_row_stride, rows) && ok(out_head_stride, heads);
+  };
+  while (piece > 1 && !divides(piece)) piece /= 2;
   return with_dtype(dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    return launch_rope<T>(p, vector, as_stream(stream));
+    return launch_rope<T>(p, piece, as_stream(stream));
   });
 }
 

@@ -102,20 +102,27 @@ __device__ __forceinline__ void Raw8<float>::set(const float* f) {
                       __float_as_uint(f[4 * i + 3]));
 }
 
-// V = 8 or 1 consecutive elements of a row.
+// V = 8, 4, 2 or 1 consecutive elements of a row, at a multiple of their size (8: of 16 bytes).
 template <typename T, int V>
-struct Piece : Raw8<T> {
-  static_assert(V == 8, "pieces hold 8 elements or 1");
+struct alignas(V * sizeof(T)) Piece {
+  T v[V];
+  __device__ __forceinline__ void load(const T* p) { *this = *reinterpret_cast<const Piece*>(p); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Piece*>(p) = *this; }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = from_f32<T>(0.f);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = to_f32(v[i]);
+  }
+  __device__ __forceinline__ void set(const float* f) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = from_f32<T>(f[i]);
+  }
 };
 template <typename T>
-struct Piece<T, 1> {
-  T v;
-  __device__ __forceinline__ void load(const T* p) { v = *p; }
-  __device__ __forceinline__ void zero() { v = from_f32<T>(0.f); }
-  __device__ __forceinline__ void store(T* p) const { *p = v; }
-  __device__ __forceinline__ void get(float* f) const { f[0] = to_f32(v); }
-  __device__ __forceinline__ void set(const float* f) { v = from_f32<T>(f[0]); }
-};
+struct Piece<T, 8> : Raw8<T> {};
 
 // Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) from global to this CTA's
 // shared memory; its bytes count towards the barrier's phase.

@@ -52,7 +52,8 @@ def run(rows, heads, dim, off, rot, layout, dtype, m=1.0, transpose=False, span=
 @pytest.mark.parametrize("rows,heads,dim,off,rot", [
     (1, 1, 2, 0, 2), (1, 1, 64, 0, 64), (3, 128, 576, 512, 64), (5, 64, 128, 0, 64), (7, 1, 576, 512, 64), (300, 1, 64, 0, 64),
     (4, 5, 100, 36, 64), (4, 3, 72, 8, 48), (6, 2, 24, 8, 8), (2, 7, 33, 5, 6), (1000, 2, 16, 0, 16), (2, 1, 1100, 40, 1024),
-    (3, 300, 1024, 0, 1024), (513, 4, 128, 64, 64)])
+    (3, 300, 1024, 0, 1024), (513, 4, 128, 64, 64), (9, 5, 100, 4, 32), (9, 3, 100, 0, 6), (9, 64, 128, 122, 6), (9, 64, 128, 3, 2),
+    (700, 3, 52, 10, 20), (9, 2, 64, 3, 50), (5, 2, 2048, 1000, 24), (3, 1, 5000, 4, 1000)])
 def test_rope(layout, dtype, rows, heads, dim, off, rot):
     run(rows, heads, dim, off, rot, layout, dtype, m=1.25, transpose=rows % 2 == 0)
 
