@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <type_traits>
 
@@ -294,104 +295,142 @@ dsa_status with_dtype(int32_t dtype, F f) {
   return f(static_cast<float*>(nullptr));
 }
 
-// Whether a [rows, cols] operand (null: absent) can be read in aligned pieces of 8 elements.
-bool wide(const void* p, int64_t ld) { return p == nullptr || (aligned(p, 16) && ld % 8 == 0); }
+// The largest piece (8, 4, 2 or 1 elements of `size` bytes) that a row of cols is made of and that every
+// operand (null: absent) holds at its alignment.
+struct Operand {
+  const void* p;
+  int64_t ld;
+};
+int piece_of(int cols, size_t size, std::initializer_list<Operand> operands, const void* codes) {
+  for (int v = 8; v > 1; v /= 2) {
+    bool ok = cols % v == 0 && aligned(codes, v);
+    for (const Operand& o : operands) ok = ok && (o.p == nullptr || (aligned(o.p, std::min<size_t>(v * size, 16)) && o.ld % v == 0));
+    if (ok) return v;
+  }
+  return 1;
+}
 
 // An output that is an input itself has its row stride too.
 bool same_rows(const void* out, int64_t ld_out, const void* in, int64_t ld_in) {
   return out == nullptr || out != in || ld_out == ld_in;
 }
 
-// Threads for a CTA-wide row of n pieces, ch per thread.
-int row_threads(int n, int ch) { return ((n + ch - 1) / ch + 31) / 32 * 32; }
+// Threads for a CTA-wide row of cols columns, ch pieces of v per thread.
+int row_threads(int cols, int v, int ch) { return (cols + 32 * v * ch - 1) / (32 * v * ch) * 32; }
 
-template <typename T, int V, int CH, bool WARP>
+template <typename T, int V, int CH, int LANES>
 dsa_status launch_rmsnorm_v(const NormParams& p, cudaStream_t s) {
-  const unsigned rows = static_cast<unsigned>(p.rows);
-  if constexpr (WARP) rmsnorm_kernel<T, V, CH, true><<<(rows + norm::kWarpRows - 1) / norm::kWarpRows, norm::kWarpRows * 32, 0, s>>>(p);
-  else rmsnorm_kernel<T, V, CH, false><<<rows, row_threads((p.cols + V - 1) / V, CH), 0, s>>>(p);
+  if constexpr (LANES > 0) {
+    constexpr int kRows = norm::kWarps * 32 / LANES;
+    rmsnorm_kernel<T, V, CH, LANES><<<static_cast<unsigned>((p.rows + kRows - 1) / kRows), norm::kWarps * 32, 0, s>>>(p);
+  } else {
+    rmsnorm_kernel<T, V, CH, 0><<<static_cast<unsigned>(p.rows), row_threads(p.cols, V, CH), 0, s>>>(p);
+  }
   return launch_status();
 }
 
-template <typename T>
-dsa_status launch_rmsnorm(const NormParams& p, bool vector, cudaStream_t s) {
-  const int n = p.cols / 8;
-  if (vector) {
-    if (n <= 32) return launch_rmsnorm_v<T, 8, 1, true>(p, s);
-    if (n <= 64) return launch_rmsnorm_v<T, 8, 2, true>(p, s);
-    if (n <= 128) return launch_rmsnorm_v<T, 8, 4, true>(p, s);
-    // few rows: as many threads as there are pieces; many: two loads in flight per thread
-    if (n <= 1024 && p.rows <= kSms) return launch_rmsnorm_v<T, 8, 1, false>(p, s);
-    if (n <= 2 * 1024) return launch_rmsnorm_v<T, 8, 2, false>(p, s);
-    if (n <= 4 * 1024) return launch_rmsnorm_v<T, 8, 4, false>(p, s);
-  } else {
-    if (p.cols <= 128) return launch_rmsnorm_v<T, 1, 4, true>(p, s);
-    if (p.cols <= 256) return launch_rmsnorm_v<T, 1, 8, true>(p, s);
-    if (p.cols <= 512) return launch_rmsnorm_v<T, 1, 16, true>(p, s);
-    if (p.cols <= 1024) return launch_rmsnorm_v<T, 1, 32, true>(p, s);
-    if (p.cols <= 8 * 1024) return launch_rmsnorm_v<T, 1, 8, false>(p, s);
-    if (p.cols <= 16 * 1024) return launch_rmsnorm_v<T, 1, 16, false>(p, s);
-  }
+// Pieces of 4, 2 or 1 elements.
+template <typename T, int V>
+dsa_status launch_rmsnorm_small(const NormParams& p, cudaStream_t s) {
+  constexpr int kMin = V == 4 ? 1 : 4 / V;  // pieces per lane that make whole groups of 128 columns
+  if (p.cols <= 128) return launch_rmsnorm_v<T, V, kMin, 32>(p, s);
+  if (p.cols <= 256) return launch_rmsnorm_v<T, V, 2 * kMin, 32>(p, s);
+  if (p.cols <= 512) return launch_rmsnorm_v<T, V, 4 * kMin, 32>(p, s);
+  if (p.cols <= 1024) return launch_rmsnorm_v<T, V, 8 * kMin, 32>(p, s);
+  if (p.cols <= 2048 * V * kMin) return launch_rmsnorm_v<T, V, 2 * kMin, 0>(p, s);
+  if (p.cols <= 4096 * V * kMin) return launch_rmsnorm_v<T, V, 4 * kMin, 0>(p, s);
   rmsnorm_general_kernel<T><<<static_cast<unsigned>(p.rows), norm::kGeneralThreads, 0, s>>>(p);
   return launch_status();
 }
 
-// CTAs of the backward, each of which writes one row of partial sums of dw: enough per SM to hide
-// a row's reduction (about 4K columns between them), at most one per row.
-int norm_bwd_per_sm(int cols) { return std::min(std::max(4096 / cols, 1), 8); }
-int64_t norm_bwd_ctas(int64_t rows, int cols) {
-  const int64_t most = static_cast<int64_t>(kSms) * norm_bwd_per_sm(cols);
+template <typename T>
+dsa_status launch_rmsnorm(const NormParams& p, int piece, cudaStream_t s) {
+  if (piece == 1) return launch_rmsnorm_small<T, 1>(p, s);
+  if (piece == 2) return launch_rmsnorm_small<T, 2>(p, s);
+  if (piece == 4) return launch_rmsnorm_small<T, 4>(p, s);
+  const int n = p.cols / 8;
+  if (n <= 8) return launch_rmsnorm_v<T, 8, 1, 8>(p, s);
+  if (n <= 16) return launch_rmsnorm_v<T, 8, 1, 16>(p, s);
+  if (n <= 32) return launch_rmsnorm_v<T, 8, 1, 32>(p, s);
+  if (n <= 64) return launch_rmsnorm_v<T, 8, 2, 32>(p, s);
+  if (n <= 128) return launch_rmsnorm_v<T, 8, 4, 32>(p, s);
+  // Few rows: as many threads as there are pieces.  Many: the loads of a whole row in flight in as few
+  // threads as its registers allow, which lets more rows share an SM (16-bit types: 4 pieces per thread,
+  // where that fills the last warp: 11502 x 3840 33.5 us against 39.6 with 2, 16384 x 8192 with residual
+  // and codes 167 against 202, but 32768 x 1536, 48 of 64 threads, 82 against 74; fp32: 2, 16384 x 4096
+  // 177 us against 196).
+  if (n <= 1024 && p.rows <= kSms) return launch_rmsnorm_v<T, 8, 1, 0>(p, s);
+  const bool four = sizeof(T) == 2 && 10 * n >= 9 * 4 * row_threads(p.cols, 8, 4);
+  if (n <= 2 * 1024 && !four) return launch_rmsnorm_v<T, 8, 2, 0>(p, s);
+  if (n <= 4 * 1024) return launch_rmsnorm_v<T, 8, 4, 0>(p, s);
+  rmsnorm_general_kernel<T><<<static_cast<unsigned>(p.rows), norm::kGeneralThreads, 0, s>>>(p);
+  return launch_status();
+}
+
+int norm_bwd_per_sm(int cols, size_t size) {
+  return static_cast<int>(std::min<int64_t>(std::max<int64_t>(16384 / (static_cast<int64_t>(cols) * size), 1), 16));
+}
+// CTAs of the backward, each of which writes one row of partial sums of dw: enough per SM to hide a
+// row's reduction (about 16 KB of rows: 32768 x 2048 bf16 88 us with 4, 100 with 2; 16384 x 4096 fp32 159
+// with 1, 172 with 2), at most one per row.
+int64_t norm_bwd_ctas(int64_t rows, int cols, size_t size) {
+  const int64_t most = static_cast<int64_t>(kSms) * norm_bwd_per_sm(cols, size);
   return rows < most ? rows : most;
 }
 
-template <typename T, int V, int CH, bool WARP>
-dsa_status launch_rmsnorm_backward_v(const NormBwdParams& p, float* dw, cudaStream_t s) {
-  int64_t ctas = norm_bwd_ctas(p.rows, p.cols);
-  if constexpr (WARP) {
-    ctas = std::min<int64_t>(std::min<int64_t>(ctas, 4 * kSms), (p.rows + norm::kWarpRows - 1) / norm::kWarpRows);
-    rmsnorm_backward_kernel<T, V, CH, true><<<static_cast<unsigned>(ctas), norm::kWarpRows * 32, 0, s>>>(p);
-  } else {
-    rmsnorm_backward_kernel<T, V, CH, false>
-        <<<static_cast<unsigned>(ctas), row_threads((p.cols + V - 1) / V, CH), 0, s>>>(p);
-  }
+dsa_status launch_dw(const NormBwdParams& p, int64_t ctas, float* dw, cudaStream_t s) {
   const dsa_status st = launch_status();
   if (st != DSA_OK) return st;
   rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 1024, 0, s>>>(p.part, static_cast<int>(ctas), p.cols, dw);
   return launch_status();
 }
 
-template <typename T>
-dsa_status launch_rmsnorm_backward(const NormBwdParams& p, bool vector, float* dw, cudaStream_t s) {
-  const int n = p.cols / 8;
-  if (vector) {
-    if (n <= 32) return launch_rmsnorm_backward_v<T, 8, 1, true>(p, dw, s);
-    if (n <= 64) return launch_rmsnorm_backward_v<T, 8, 2, true>(p, dw, s);
-    const int64_t stage = static_cast<int64_t>(p.cols) * sizeof(T) * (p.dres != nullptr ? 3 : 2);
-    const int stages = static_cast<int>(std::min<int64_t>(norm::kRingBytes / norm_bwd_per_sm(p.cols) / stage, norm::kRingMax));
-    if (n <= 1024 && stages >= 2) {
-      const int64_t ctas = norm_bwd_ctas(p.rows, p.cols);
-      const int smem = static_cast<int>(stages * stage);
-      if (cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return DSA_ERR_CUDA;
-      rmsnorm_backward_ring_kernel<T><<<static_cast<unsigned>(ctas), row_threads(n, 1), smem, s>>>(p, stages);
-      const dsa_status st = launch_status();
-      if (st != DSA_OK) return st;
-      rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 1024, 0, s>>>(p.part, static_cast<int>(ctas), p.cols, dw);
-      return launch_status();
-    }
-    if (n <= 2 * 1024) return launch_rmsnorm_backward_v<T, 8, 2, false>(p, dw, s);
+template <typename T, int V, int CH, int LANES>
+dsa_status launch_rmsnorm_backward_v(const NormBwdParams& p, float* dw, cudaStream_t s) {
+  int64_t ctas = norm_bwd_ctas(p.rows, p.cols, sizeof(T));
+  if constexpr (LANES > 0) {
+    constexpr int kRows = norm::kWarps * 32 / LANES;
+    ctas = std::min<int64_t>(std::min<int64_t>(ctas, 4 * kSms), (p.rows + kRows - 1) / kRows);
+    rmsnorm_backward_kernel<T, V, CH, LANES><<<static_cast<unsigned>(ctas), norm::kWarps * 32, 0, s>>>(p);
   } else {
-    if (p.cols <= 128) return launch_rmsnorm_backward_v<T, 1, 4, true>(p, dw, s);
-    if (p.cols <= 512) return launch_rmsnorm_backward_v<T, 1, 16, true>(p, dw, s);
-    if (p.cols <= 4 * 1024) return launch_rmsnorm_backward_v<T, 1, 4, false>(p, dw, s);
-    if (p.cols <= 8 * 1024) return launch_rmsnorm_backward_v<T, 1, 8, false>(p, dw, s);
+    rmsnorm_backward_kernel<T, V, CH, 0><<<static_cast<unsigned>(ctas), row_threads(p.cols, V, CH), 0, s>>>(p);
   }
-  const int64_t ctas = norm_bwd_ctas(p.rows, p.cols);
+  return launch_dw(p, ctas, dw, s);
+}
+
+template <typename T, int V>
+dsa_status launch_rmsnorm_backward_small(const NormBwdParams& p, float* dw, cudaStream_t s) {
+  constexpr int kMin = 4 / V;  // pieces of 128 columns
+  if (p.cols <= 128) return launch_rmsnorm_backward_v<T, V, kMin, 32>(p, dw, s);
+  if (p.cols <= 4096) return launch_rmsnorm_backward_v<T, V, kMin, 0>(p, dw, s);
+  if (p.cols <= 8192) return launch_rmsnorm_backward_v<T, V, 2 * kMin, 0>(p, dw, s);
+  const int64_t ctas = norm_bwd_ctas(p.rows, p.cols, sizeof(T));
   rmsnorm_backward_general_kernel<T><<<static_cast<unsigned>(ctas), norm::kGeneralThreads, 0, s>>>(p);
-  const dsa_status st = launch_status();
-  if (st != DSA_OK) return st;
-  rmsnorm_dw_kernel<<<(p.cols + 31) / 32, 1024, 0, s>>>(p.part, static_cast<int>(ctas), p.cols, dw);
-  return launch_status();
+  return launch_dw(p, ctas, dw, s);
+}
+
+template <typename T>
+dsa_status launch_rmsnorm_backward(const NormBwdParams& p, int piece, float* dw, cudaStream_t s) {
+  if (piece == 1) return launch_rmsnorm_backward_small<T, 1>(p, dw, s);
+  if (piece == 2) return launch_rmsnorm_backward_small<T, 2>(p, dw, s);
+  if (piece == 4) return launch_rmsnorm_backward_small<T, 4>(p, dw, s);
+  const int n = p.cols / 8;
+  if (n <= 8) return launch_rmsnorm_backward_v<T, 8, 1, 8>(p, dw, s);
+  if (n <= 16) return launch_rmsnorm_backward_v<T, 8, 1, 16>(p, dw, s);
+  if (n <= 32) return launch_rmsnorm_backward_v<T, 8, 1, 32>(p, dw, s);
+  const int64_t stage = static_cast<int64_t>(p.cols) * sizeof(T) * (p.dres != nullptr ? 3 : 2);
+  const int stages = static_cast<int>(std::min<int64_t>(norm::kRingBytes / norm_bwd_per_sm(p.cols, sizeof(T)) / stage, norm::kRingMax));
+  const int64_t ctas = norm_bwd_ctas(p.rows, p.cols, sizeof(T));
+  if (n <= 1024 && stages >= 2) {
+    const int smem = static_cast<int>(stages * stage);
+    if (cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return DSA_ERR_CUDA;
+    rmsnorm_backward_ring_kernel<T><<<static_cast<unsigned>(ctas), row_threads(p.cols, 8, 1), smem, s>>>(p, stages);
+    return launch_dw(p, ctas, dw, s);
+  }
+  if (n <= 2 * 1024) return launch_rmsnorm_backward_v<T, 8, 2, 0>(p, dw, s);
+  rmsnorm_backward_general_kernel<T><<<static_cast<unsigned>(ctas), norm::kGeneralThreads, 0, s>>>(p);
+  return launch_dw(p, ctas, dw, s);
 }
 
 // piece: elements that heads, strides and pointers divide into (8, 4, 2 or 1).
@@ -1048,17 +1087,16 @@ dsa_status dsa_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_
   p.scale = scale;
   p.groups = group == 0 ? 0 : cols / DSA_QUANT_GROUP + (cols % DSA_QUANT_GROUP != 0);
   p.rstd = rstd;
-  const bool vector = cols % 8 == 0 && wide(x, ld_x) && wide(residual, ld_residual) && wide(weight, 0) && wide(y, ld_y) &&
-                      wide(residual_out, ld_residual_out) && aligned(codes, 8);
+  const int piece = piece_of(cols, es, {{x, ld_x}, {residual, ld_residual}, {weight, 0}, {y, ld_y}, {residual_out, ld_residual_out}}, codes);
   return with_dtype(dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    return launch_rmsnorm<T>(p, vector, as_stream(stream));
+    return launch_rmsnorm<T>(p, piece, as_stream(stream));
   });
 }
 
 size_t dsa_rmsnorm_backward_workspace_size(int64_t rows, int32_t cols) {
   if (rows <= 0 || cols <= 0) return 0;
-  return align256(static_cast<size_t>(norm_bwd_ctas(rows, cols)) * cols * sizeof(float));
+  return align256(static_cast<size_t>(norm_bwd_ctas(rows, cols, 2)) * cols * sizeof(float));
 }
 
 dsa_status dsa_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* weight,
@@ -1095,11 +1133,10 @@ dsa_status dsa_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, in
   p.cols = cols;
   p.dh = dh;
   p.part = static_cast<float*>(workspace);
-  const bool vector = cols % 8 == 0 && wide(dy, ld_dy) && wide(h, ld_h) && wide(weight, 0) && wide(dresidual, ld_dresidual) &&
-                      wide(dh, ld_dh);
+  const int piece = piece_of(cols, es, {{dy, ld_dy}, {h, ld_h}, {weight, 0}, {dresidual, ld_dresidual}, {dh, ld_dh}}, nullptr);
   return with_dtype(dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    return launch_rmsnorm_backward<T>(p, vector, dw, s);
+    return launch_rmsnorm_backward<T>(p, piece, dw, s);
   });
 }
 

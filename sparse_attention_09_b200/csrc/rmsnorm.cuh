@@ -8,11 +8,12 @@
 //
 // HBM-bound: a row is read once and kept in registers (as fp32 h) between the sum of squares, the
 // maximum of its codes and the writes.  A row belongs to one CTA, or, up to 1024 columns, to one
-// warp (no block barrier; eight rows per CTA).  Rows that are not made of aligned 8-element pieces
-// use the same kernels with single elements.  Rows too wide for the registers of a CTA take the
-// general kernels, which read a row again for each pass (from L1 / L2).
-// Measured on 32768 x 4096 bf16 with residual, y and codes: 185 us (6.5 TB/s, 0.99 of measured HBM;
-// 193 us with a division per code).
+// warp or a half or quarter of one (no block barrier).  Rows that are not made of aligned pieces of 8
+// elements use the same kernels with pieces of 4, 2 or 1.  Rows too wide for the registers of a CTA take
+// the general kernels, which read a row again for each pass (from L1 / L2).
+// Measured on 32768 x 4096 bf16 with residual, y and codes: 180 us (6.7 TB/s, 1.02 of measured HBM's copy
+// rate; 193 us with a division per code, 185 with 2 pieces per thread); 65536 x 128 bf16 9.3 us (half a
+// warp per row; a warp, half of it idle: 14.9).
 #pragma once
 
 #include "elem.cuh"
@@ -52,35 +53,54 @@ struct NormBwdParams {
 namespace norm {
 
 constexpr int kGroup = DSA_QUANT_GROUP;
-constexpr int kWarpRows = 8;       // rows per CTA of the warp-per-row kernels
-constexpr int kWarpCols = 1024;    // widest row of one warp: 4 pieces of 8 elements per lane
+constexpr int kWarps = 8;          // warps per CTA where a row is part of a warp's work
 constexpr int kGeneralThreads = 256;
 constexpr int kRingMax = 8;        // stages of the backward's ring
 constexpr int kRingBytes = 200 * 1024;  // shared memory for the rings of an SM's CTAs
 
-// Writes the codes of V values (8: at an 8-byte boundary).
+// Writes the codes of V values, at a multiple of V bytes.
 template <int V>
 __device__ __forceinline__ void encode(uint8_t* dst, const float* v, float s) {
   const float inv = quant::inverse_of(s);
   auto q = [&](int i) { return quant::over(v[i], s, inv); };
   if constexpr (V == 1) {
     *dst = static_cast<uint8_t>(quant::to_e4m3x2(q(0), 0.f));
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<uint16_t*>(dst) = quant::to_e4m3x2(q(0), q(1));
   } else {
-    uint32_t out[2];
+    uint32_t out[V / 4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < V / 4; ++i) {
       const uint32_t lo = quant::to_e4m3x2(q(4 * i), q(4 * i + 1));
       const uint32_t hi = quant::to_e4m3x2(q(4 * i + 2), q(4 * i + 3));
       out[i] = lo | (hi << 16);
     }
-    *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+    if constexpr (V == 4) *reinterpret_cast<uint32_t*>(dst) = out[0];
+    else *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
   }
 }
 
-// First column of piece i of thread t of a row's nt threads.
+// First column of piece i of thread t of a row's nt threads.  Pieces of 8: the row's piece t + i nt;
+// smaller ones: a warp has 32 CH V consecutive columns, 32 V to a piece index, so that the 128 columns
+// of a group belong to one warp.
 template <int V, int CH>
 __device__ __forceinline__ int column(int t, int nt, int i) {
-  return V == 8 ? 8 * (t + i * nt) : (t >> 5) * (32 * CH) + 32 * i + (t & 31);
+  return V == 8 ? 8 * (t + i * nt) : (t >> 5) * (32 * V * CH) + 32 * V * i + V * (t & 31);
+}
+
+// Sum / maximum over the LANES lanes of a row (LANES = 8, 16 or 32 neighbours).
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {  // of non-negative values
+  if constexpr (LANES == 32) return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
 
 // Block-wide sum / maximum; every thread calls it and gets the result.  red holds one float per
@@ -102,18 +122,20 @@ __device__ __forceinline__ float block_reduce(float v, float* red) {
 
 }  // namespace norm
 
-// CH pieces of V elements per thread (threads per row: whole warps).  Pieces of 8: piece i of thread
-// t is the row's piece t + i * threads.  Pieces of 1, for rows that are not made of aligned pieces
-// of 8: a warp has 32 CH consecutive columns, 32 to a piece index.
-template <typename T, int V, int CH, bool WARP>
-__global__ void __launch_bounds__(WARP ? norm::kWarpRows * 32 : 1024) rmsnorm_kernel(const NormParams p) {
+// CH pieces of V elements per thread; a row belongs to LANES lanes of a warp (8, 16 or 32), or to the
+// CTA (LANES = 0).
+template <typename T, int V, int CH, int LANES>
+__global__ void __launch_bounds__(LANES > 0 ? norm::kWarps * 32 : 1024) rmsnorm_kernel(const NormParams p) {
   using elem::Piece;
+  constexpr bool kCta = LANES == 0;
+  constexpr int kLanes = kCta ? 32 : LANES;
   __shared__ float red[2][32];
-  const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int nt = WARP ? 32 : blockDim.x;
-  const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * norm::kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
-  if (WARP && row >= p.rows) return;
+  const int t = kCta ? threadIdx.x : threadIdx.x % kLanes;
+  const int nt = kCta ? blockDim.x : kLanes;
+  const int64_t row = kCta ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * (norm::kWarps * 32 / kLanes) + threadIdx.x / kLanes;
+  const bool live = kCta || row < p.rows;
   auto col = [&](int i) { return norm::column<V, CH>(t, nt, i); };
+  auto has = [&](int i) { return live && col(i) < p.cols; };
   const T* x = static_cast<const T*>(p.x) + row * p.ld_x;
   const T* res = p.res != nullptr ? static_cast<const T*>(p.res) + row * p.ld_res : nullptr;
   float h[CH][V];
@@ -124,7 +146,7 @@ __global__ void __launch_bounds__(WARP ? norm::kWarpRows * 32 : 1024) rmsnorm_ke
     for (int i = 0; i < CH; ++i) {
       a[i].zero();
       b[i].zero();
-      if (col(i) < p.cols) {
+      if (has(i)) {
         a[i].load(x + col(i));
         if (res != nullptr) b[i].load(res + col(i));
       }
@@ -149,16 +171,15 @@ __global__ void __launch_bounds__(WARP ? norm::kWarpRows * 32 : 1024) rmsnorm_ke
     wr[i].zero();
     if (col(i) < p.cols) wr[i].load(w + col(i));
   }
-  ss = WARP ? elem::warp_sum(ss) : norm::block_reduce<false>(ss, red[0]);
+  ss = kCta ? norm::block_reduce<false>(ss, red[0]) : norm::lanes_sum<kLanes>(ss);
   const float rs = __fdiv_rn(1.f, sqrtf(__fdiv_rn(ss, static_cast<float>(p.cols)) + p.eps));
-  if (p.rstd != nullptr && t == 0) p.rstd[row] = rs;
+  if (p.rstd != nullptr && t == 0 && live) p.rstd[row] = rs;
   T* ro = p.res_out != nullptr ? static_cast<T*>(p.res_out) + row * p.ld_ro : nullptr;
   T* y = p.y != nullptr ? static_cast<T*>(p.y) + row * p.ld_y : nullptr;
   float amax[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const bool in = col(i) < p.cols;
-    if (ro != nullptr && in) {
+    if (ro != nullptr && has(i)) {
       Piece<T, V> o;
       o.set(h[i]);
       o.store(ro + col(i));
@@ -171,7 +192,7 @@ __global__ void __launch_bounds__(WARP ? norm::kWarpRows * 32 : 1024) rmsnorm_ke
       h[i][j] = h[i][j] * rs * g[j];
       amax[i] = fmaxf(amax[i], fabsf(h[i][j]));  // a NaN never wins fmaxf
     }
-    if (y != nullptr && in) {
+    if (y != nullptr && has(i)) {
       Piece<T, V> o;
       o.set(h[i]);
       o.store(y + col(i));
@@ -183,37 +204,26 @@ __global__ void __launch_bounds__(WARP ? norm::kWarpRows * 32 : 1024) rmsnorm_ke
     float m = amax[0];
 #pragma unroll
     for (int i = 1; i < CH; ++i) m = fmaxf(m, amax[i]);
-    m = WARP ? __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))) : norm::block_reduce<true>(m, red[1]);
+    m = kCta ? norm::block_reduce<true>(m, red[1]) : norm::lanes_max<kLanes>(m);
     const float s = quant::scale_of(m);
-    if (t == 0) p.scale[row] = s;
+    if (t == 0 && live) p.scale[row] = s;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
-      if (col(i) < p.cols) norm::encode<V>(codes + col(i), h[i], s);
-  } else if constexpr (V == 8) {
-    // a group of 128 columns is 16 pieces: 16 neighbouring lanes
+      if (has(i)) norm::encode<V>(codes + col(i), h[i], s);
+  } else {
+    // a group of 128 columns: 16 neighbouring lanes of one piece index (V = 8), or all lanes of kPer of them
+    constexpr int kPer = V >= 4 ? 1 : 4 / V;
+    static_assert(CH % kPer == 0, "groups do not cross threads' ranges");
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = col(i);
+    for (int i = 0; i < CH; i += kPer) {
       float m = amax[i];
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float s = quant::scale_of(m);
-      if (c < p.cols) {
-        if (c % norm::kGroup == 0) p.scale[row * p.groups + c / norm::kGroup] = s;
-        norm::encode<V>(codes + c, h[i], s);
-      }
-    }
-  } else {
-    // a group is four consecutive piece indexes of one warp
-    static_assert(V == 8 || CH % 4 == 0, "groups do not cross threads' ranges");
+      for (int j = i + 1; j < i + kPer; ++j) m = fmaxf(m, amax[j]);
+      const float s = quant::scale_of(norm::lanes_max<V == 8 ? (kLanes < 16 ? kLanes : 16) : 32>(m));
+      if (has(i) && col(i) % norm::kGroup == 0) p.scale[row * p.groups + col(i) / norm::kGroup] = s;
 #pragma unroll
-    for (int i = 0; i < CH; i += 4) {
-      const float m4 = fmaxf(fmaxf(amax[i], amax[i + 1]), fmaxf(amax[i + 2], amax[i + 3]));
-      const float s = quant::scale_of(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m4))));
-      if ((t & 31) == 0 && col(i) < p.cols) p.scale[row * p.groups + col(i) / norm::kGroup] = s;
-#pragma unroll
-      for (int j = i; j < i + 4; ++j)
-        if (col(j) < p.cols) norm::encode<V>(codes + col(j), h[j], s);
+      for (int j = i; j < i + kPer; ++j)
+        if (has(j)) norm::encode<V>(codes + col(j), h[j], s);
     }
   }
 }
@@ -282,16 +292,18 @@ __global__ void __launch_bounds__(norm::kGeneralThreads) rmsnorm_general_kernel(
   }
 }
 
-// Backward: a persistent grid; each row group (a CTA, or each warp of it) keeps its columns' weights
-// and its partial sums of dw in registers over all of its rows, and issues a row's loads before it
-// reduces and writes the row before.
-template <typename T, int V, int CH, bool WARP>
-__global__ void __launch_bounds__(WARP ? norm::kWarpRows * 32 : 1024) rmsnorm_backward_kernel(const NormBwdParams p) {
+// Backward: a persistent grid; each row group (a CTA, or LANES lanes of a warp) keeps its columns'
+// weights and its partial sums of dw in registers over all of its rows, and issues a row's loads before
+// it reduces and writes the row before.
+template <typename T, int V, int CH, int LANES>
+__global__ void __launch_bounds__(LANES > 0 ? norm::kWarps * 32 : 1024) rmsnorm_backward_kernel(const NormBwdParams p) {
   using elem::Piece;
+  constexpr bool kCta = LANES == 0;
+  constexpr int kLanes = kCta ? 32 : LANES;
   __shared__ float red[2][32];
-  __shared__ float dwx[WARP ? norm::kWarpRows * 256 : 1];
-  const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int nt = WARP ? 32 : blockDim.x;
+  __shared__ float dwx[kCta ? 1 : norm::kWarps * 256];
+  const int t = kCta ? threadIdx.x : threadIdx.x % kLanes;
+  const int nt = kCta ? blockDim.x : kLanes;
   auto col = [&](int i) { return norm::column<V, CH>(t, nt, i); };
   const T* dyp = static_cast<const T*>(p.dy);
   const T* hp = static_cast<const T*>(p.h);
@@ -306,7 +318,8 @@ __global__ void __launch_bounds__(WARP ? norm::kWarpRows * 32 : 1024) rmsnorm_ba
     for (int j = 0; j < V; ++j) dw[i][j] = 0.f;
   }
   const float inv_cols = 1.f / static_cast<float>(p.cols);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (WARP ? norm::kWarpRows : 1);
+  constexpr int kRows = kCta ? 1 : norm::kWarps * 32 / kLanes;  // of a CTA
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
   Piece<T, V> a[CH], b[CH], d[CH];
   float rs = 0.f;
   auto load_row = [&](int64_t row, Piece<T, V>* pa, Piece<T, V>* pb, Piece<T, V>* pd, float& r) {
@@ -324,9 +337,12 @@ __global__ void __launch_bounds__(WARP ? norm::kWarpRows * 32 : 1024) rmsnorm_ba
     if (row < p.rows) r = p.rstd[row];
   };
   int it = 0;
-  int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * norm::kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
-  load_row(row, a, b, d, rs);
-  for (; row < p.rows; row += step, ++it) {
+  // base: the first row of the CTA's step, the same for all lanes of a warp
+  int64_t base = static_cast<int64_t>(blockIdx.x) * kRows;
+  const int mine = kCta ? 0 : threadIdx.x / kLanes;
+  load_row(base + mine, a, b, d, rs);
+  for (; base < p.rows; base += step, ++it) {
+    const int64_t row = base + mine;
     Piece<T, V> na[CH], nb[CH], nd[CH];
     float nrs = 0.f;
     load_row(row + step, na, nb, nd, nrs);
@@ -344,11 +360,11 @@ __global__ void __launch_bounds__(WARP ? norm::kWarpRows * 32 : 1024) rmsnorm_ba
         dw[i][j] = fmaf(u, rs, dw[i][j]);
       }
     }
-    dot = WARP ? elem::warp_sum(dot) : norm::block_reduce<false>(dot, red[it & 1]);
+    dot = kCta ? norm::block_reduce<false>(dot, red[it & 1]) : norm::lanes_sum<kLanes>(dot);
     const float k = dot * inv_cols * rs * rs;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      if (col(i) < p.cols) {
+      if (row < p.rows && col(i) < p.cols) {
         float dy[V], h[V], wf[V], r[V], o[V];
         a[i].get(dy);
         b[i].get(h);
@@ -367,23 +383,30 @@ __global__ void __launch_bounds__(WARP ? norm::kWarpRows * 32 : 1024) rmsnorm_ba
     rs = nrs;
   }
   float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.cols;
-  if constexpr (WARP) {
-    // the eight warps' sums, added in warp order, 256 columns at a time
-    constexpr int kPer = 256 / (32 * V);  // piece indexes that make 256 columns
-    constexpr int kStep = kPer < 1 ? 1 : kPer;
+  if constexpr (!kCta) {
+    // the warp's row groups, then the eight warps in their order, 256 columns at a time
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int o = 16; o >= kLanes; o >>= 1) dw[i][j] += __shfl_xor_sync(0xffffffffu, dw[i][j], o);
+    constexpr int kStep = 256 / (32 * V) < 1 ? 1 : 256 / (32 * V);  // piece indexes that make 256 columns
 #pragma unroll
     for (int i0 = 0; i0 < CH; i0 += kStep) {
       __syncthreads();
+      if ((threadIdx.x & 31) < kLanes) {
 #pragma unroll
-      for (int i = i0; i < i0 + kStep && i < CH; ++i)
+        for (int i = i0; i < i0 + kStep && i < CH; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) dwx[(threadIdx.x >> 5) * 256 + (col(i) + j) % 256] = dw[i][j];
+          for (int j = 0; j < V; ++j) dwx[(threadIdx.x >> 5) * 256 + (col(i) + j) % 256] = dw[i][j];
+      }
       __syncthreads();
-      const int c = (V == 8 ? 256 * i0 : 32 * i0) + static_cast<int>(threadIdx.x);
-      if (c < p.cols && c < 32 * V * CH) {
+      const int c = 32 * V * i0 + static_cast<int>(threadIdx.x);
+      if (c < p.cols && c < kLanes * V * CH) {
         float s = 0.f;
 #pragma unroll
-        for (int v = 0; v < norm::kWarpRows; ++v) s += dwx[v * 256 + threadIdx.x];
+        for (int v = 0; v < norm::kWarps; ++v) s += dwx[v * 256 + threadIdx.x];
         part[c] = s;
       }
     }
