@@ -423,7 +423,9 @@ dsa_status launch_rmsnorm_backward(const NormBwdParams& p, int piece, float* dw,
   const int64_t ctas = norm_bwd_ctas(p.rows, p.cols, sizeof(T));
   if (n <= 1024 && stages >= 2) {
     const int smem = static_cast<int>(stages * stage);
-    if (cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    // the same limit for every size, so that calls from several host threads do not lower one another's
+    if (cudaFuncSetAttribute(rmsnorm_backward_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, norm::kRingBytes) !=
+        cudaSuccess)
       return DSA_ERR_CUDA;
     rmsnorm_backward_ring_kernel<T><<<static_cast<unsigned>(ctas), row_threads(p.cols, 8, 1), smem, s>>>(p, stages);
     return launch_dw(p, ctas, dw, s);

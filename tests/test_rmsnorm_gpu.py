@@ -271,6 +271,34 @@ def test_another_stream_and_a_captured_graph():
     assert torch.equal(dh, eager[0]) and torch.equal(b, eager[1])
 
 
+def test_calls_from_several_threads():
+    """Different sizes at once, each on its own stream with its own workspace."""
+    import threading
+
+    cases, errors = [], []
+    for i, cols in enumerate((512, 2048, 5120, 8192)):
+        dy, h, w = rnd((300, cols), torch.bfloat16, i), rnd((300, cols), torch.bfloat16, 9 + i), rnd((cols,), torch.bfloat16, 3)
+        rstd = (h.double().square().mean(1) + EPS).rsqrt().float()
+        cases.append((dy, h, w, rstd, backward(dy, h, w, rstd)))
+    torch.cuda.synchronize()
+
+    def work(dy, h, w, rstd, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    dh, dw = backward(dy, h, w, rstd)
+                    assert torch.equal(dh, want[0]) and torch.equal(dw, want[1])
+        except BaseException as e:  # noqa: BLE001 (shown by the assertion below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
 def test_wrapper_refusals():
     x, w = torch.zeros((4, 64), device="cuda"), torch.zeros(64, device="cuda")
     for kw in (dict(y=x.half()), dict(y=x[:, :32]), dict(y=x, residual=x[:2]), dict(y=x, rstd=torch.zeros(5, device="cuda")),
