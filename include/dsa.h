@@ -485,7 +485,7 @@ dsa_status dsa_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling, 
  * A row whose sequence, position (>= max_seqlen) or block is out of range is skipped and sets
  * DSA_ERR_DEVICE_CHECK.  Rows must name distinct (sequence, position) slots, and no two
  * sequences share a page that is written: which row's values a slot named twice keeps is not defined.
- * Slots that no row names are not touched.  rows == 0 is a no-op.
+ * Slots that no row names are not touched.  kv and key lie outside the caches.  rows == 0 is a no-op.
  * DSA_ERR_INVALID_ARGUMENT: NULL pointers, kv not 16-byte aligned or ld_kv no multiple of 8, key not
  * 4-byte aligned or ld_key odd, key_rot_offset odd or outside [0, d_I - 64], caches misaligned
  * (latent data 16 bytes, key data 2), inconsistent sizes; DSA_ERR_UNSUPPORTED: d_I not 64 or 128,

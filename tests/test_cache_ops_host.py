@@ -207,3 +207,25 @@ def test_wrappers_refuse_tensors_they_cannot_pass_on():
         dsa.dsa_window_mla_prefill(q, lat, 1, 16, 4, 0, 0.04, out)
     with pytest.raises(ValueError):
         dsa.dsa_window_mla_decode(q, lat, 4, 16, 4, 0, 0.04, out)
+
+
+def test_wrappers_refuse_what_is_no_tensor_or_does_not_fit():
+    x, w = torch.zeros(4, 8), torch.zeros(8)
+    with pytest.raises(ValueError, match="x must be a tensor"):
+        dsa.dsa_rmsnorm([1.0], w, 1e-6, y=x)
+    with pytest.raises(ValueError, match="x must be a tensor"):
+        dsa.dsa_rope(None, None, None, x, 0, 8)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        dsa.dsa_rmsnorm(x, w, "no number", y=x)  # the tensors are looked at first
+    with pytest.raises(ValueError, match="takes 10 arguments"):
+        dsa._marshal.rmsnorm(x, w)
+    lat = dsa.contiguous_desc(torch.zeros(4, 576, dtype=torch.bfloat16), torch.tensor([0, 4], dtype=torch.int32), 4)
+    q, out = torch.zeros(4, 16, 576, dtype=torch.bfloat16), torch.zeros(4, 16, 512, dtype=torch.bfloat16)
+    for B in (0, 2, -1):
+        with pytest.raises(ValueError, match="sequences"):
+            dsa.dsa_window_mla_prefill(q, lat, B, 16, 4, 0, 0.04, out)
+    bad = dsa.contiguous_desc(torch.zeros(4, 576, dtype=torch.bfloat16), torch.tensor([0, 4]), 4)
+    with pytest.raises(ValueError, match="int32"):
+        dsa.dsa_window_mla_prefill(q, bad, 1, 16, 4, 0, 0.04, out)
+    with pytest.raises(ValueError, match="rows of 576"):
+        dsa.dsa_window_mla_prefill(q, dsa.contiguous_desc(torch.zeros(4, 576), lat._refs[2], 4), 1, 16, 4, 0, 0.04, out)

@@ -313,6 +313,10 @@ def test_wrapper_refusals():
         dsa.dsa_window_mla_decode(q, desc, 1, 128, 100, 0, 0.0, out)
     with pytest.raises(dsa.DSAError):
         dsa.dsa_window_mla_prefill(q, desc, 1, 128, 10, 0, SM, out)  # paged
+    for window, sinks, scale, kind in ((2 ** 31, 0, SM, ValueError), (10, -2 ** 40, SM, ValueError), (4.5, 0, SM, TypeError),
+                                       (10, 0, "a", TypeError)):
+        with pytest.raises(kind):
+            dsa.dsa_window_mla_decode(q, desc, 1, 128, window, sinks, scale, out)
     flat = dsa.contiguous_desc(latent.flatten(0, 1), torch.tensor([0, 64], dtype=torch.int32, device="cuda"), 64)
     with pytest.raises(ValueError):
         dsa.dsa_window_mla_prefill(q, flat, 1, 128, 10, 0, SM, out)  # as many queries as tokens
