@@ -390,6 +390,16 @@ def _cache(where, name, desc, dtype, width, dev):
         raise ValueError(f"{where}: {name} must describe {dtype} rows of {width}, got {data.dtype} {tuple(data.shape)}")
     if scale is not None and (scale.dtype is not torch.float32 or scale.shape != data.shape[:-1]):
         raise ValueError(f"{where}: {name} must have one fp32 scale per row, got {scale.dtype} {tuple(scale.shape)}")
+    s = desc.struct
+    paged = s.kind == DSA_KV_PAGED
+    rows = s.num_blocks * s.block_size if paged else s.total_tokens
+    if data.numel() != rows * width:
+        raise ValueError(f"{where}: {name} must describe {'[blocks, block size' if paged else '[tokens'}, {width}] data, got "
+                         f"{tuple(data.shape)}")
+    lengths = (desc.batch * s.max_blocks_per_seq, desc.batch) if paged else (desc.batch + 1,)
+    if desc.batch < 1 or any(t.numel() != n for t, n in zip(tables, lengths)):
+        raise ValueError(f"{where}: the tables and lengths that {name} describes must have one entry per sequence (cu_seqlens "
+                         f"one more), got {[tuple(t.shape) for t in tables]}")
     for t in (data, scale, *tables):
         if t is not None and (not t.is_contiguous() or t.get_device() != dev):
             raise ValueError(f"{where}: the tensors that {name} describes must be contiguous, on the current device")

@@ -229,3 +229,36 @@ def test_wrappers_refuse_what_is_no_tensor_or_does_not_fit():
         dsa.dsa_window_mla_prefill(q, bad, 1, 16, 4, 0, 0.04, out)
     with pytest.raises(ValueError, match="rows of 576"):
         dsa.dsa_window_mla_prefill(q, dsa.contiguous_desc(torch.zeros(4, 576), lat._refs[2], 4), 1, 16, 4, 0, 0.04, out)
+
+
+@pytest.mark.parametrize("data,table,ctx", [
+    ((10, 576), (2, 4), (2,)),          # no page dimension: its 576 would be taken for the page size
+    ((10, 64, 2, 576), (2, 4), (2,)),   # two rows per slot
+    ((10, 64, 576), (2, 4), (1,)),      # fewer lengths than sequences
+    ((10, 64, 576), (2, 4), (3,)),
+    ((10, 64, 576), (0, 4), (0,)),
+    ((10, 64, 576), (2, 4, 2), (2,))])
+def test_wrappers_refuse_descriptors_that_do_not_fit_their_tensors(data, table, ctx):
+    desc = dsa.paged_desc(torch.zeros(data, dtype=torch.bfloat16), torch.zeros(table, dtype=torch.int32),
+                          torch.zeros(ctx, dtype=torch.int32), 256)
+    B = table[0]
+    q, out = torch.zeros(B, 16, 576, dtype=torch.bfloat16), torch.zeros(B, 16, 512, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="latent"):
+        dsa.dsa_window_mla_decode(q, desc, B, 16, 8, 0, 0.04, out)
+    with pytest.raises(ValueError, match="latent"):
+        dsa.dsa_cache_append(torch.zeros(B, 576), None, 1e-6, None, None, torch.zeros(B, dtype=torch.int32), None, desc, None)
+
+
+def test_wrappers_refuse_packed_lengths_of_another_rank():
+    for cu in ((2, 2), (1,)):
+        desc = dsa.contiguous_desc(torch.zeros(4, 576, dtype=torch.bfloat16), torch.zeros(cu, dtype=torch.int32), 4)
+        with pytest.raises(ValueError, match="latent"):
+            dsa.dsa_window_mla_prefill(torch.zeros(4, 16, 576), desc, desc.batch, 16, 8, 0, 0.04, torch.zeros(4, 16, 512))
+
+
+def test_wrappers_take_a_head_dimension_of_one():
+    """[blocks, 64, 1, 576], as caches with a head dimension are laid out: the rows are the same."""
+    desc = dsa.paged_desc(torch.zeros(3, 64, 1, 576, dtype=torch.bfloat16), torch.zeros(2, 4, dtype=torch.int32),
+                          torch.zeros(2, dtype=torch.int32), 256)
+    with pytest.raises(ValueError, match="current CUDA device"):  # refused for being on the CPU, not for its shape
+        dsa.dsa_window_mla_decode(torch.zeros(2, 16, 576), desc, 2, 16, 8, 0, 0.04, torch.zeros(2, 16, 512))
