@@ -408,7 +408,8 @@ typedef enum { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_NTK = 2, DSA_RO
  * element-aligned pointers and strides (16-byte aligned pointers with strides and cols that are
  * multiples of 8 take the wide-load path).  rows == 0 is a no-op.
  * DSA_ERR_INVALID_ARGUMENT: NULL or misaligned pointers, sizes or strides as above, group not 0 or
- * DSA_QUANT_GROUP, eps negative or not finite, unknown dtype; DSA_ERR_UNSUPPORTED: rows > 2^31 - 1.
+ * DSA_QUANT_GROUP, eps negative or not finite, unknown dtype; DSA_ERR_UNSUPPORTED: rows > 2^31 - 1 or
+ * cols > 2^30.
  */
 dsa_status dsa_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual, const void* weight,
                        int64_t rows, int32_t cols, int32_t dtype, float eps, void* y, int64_t ld_y,
@@ -445,8 +446,8 @@ size_t dsa_rmsnorm_backward_workspace_size(int64_t rows, int32_t cols);
  * the device.  Computed in fp32, rounded once.
  * rows == 0 or heads == 0 is a no-op.  DSA_ERR_INVALID_ARGUMENT: NULL or misaligned pointers,
  * rot_dim odd or < 2, a range outside the head, strides as above, unknown layout or dtype, mscale
- * not finite, out == x with other strides; DSA_ERR_UNSUPPORTED: rot_dim > 1024, or rows or
- * heads * dim above 2^31 - 1.
+ * not finite, out == x with other strides; DSA_ERR_UNSUPPORTED: rot_dim > 1024, rows above
+ * 2^31 - 1, or heads * dim above 2^30.
  */
 dsa_status dsa_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride, void* out, int64_t out_row_stride,
                     int64_t out_head_stride, int64_t rows, int32_t heads, int32_t dim, int32_t rot_offset,
@@ -482,8 +483,8 @@ dsa_status dsa_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling, 
  * paged, position p of sequence b is row block_table[b, p/64] * 64 + p % 64; contiguous, row
  * cu_seqlens[b] + p, which must lie before cu_seqlens[b+1].  context_lens is not read.  Either half may be
  * left out: kv and latent NULL, or key and keys NULL.  A row with seq -1 is padding and skipped.
- * A row whose sequence, position (>= max_seqlen) or block is out of range is skipped and sets
- * DSA_ERR_DEVICE_CHECK.  Rows must name distinct (sequence, position) slots, and no two
+ * A row whose sequence, position (>= max_seqlen) or block is out of range in a cache is skipped there
+ * and sets DSA_ERR_DEVICE_CHECK.  Rows must name distinct (sequence, position) slots, and no two
  * sequences share a page that is written: which row's values a slot named twice keeps is not defined.
  * Slots that no row names are not touched.  kv and key lie outside the caches.  rows == 0 is a no-op.
  * DSA_ERR_INVALID_ARGUMENT: NULL pointers, kv not 16-byte aligned or ld_kv no multiple of 8, key not

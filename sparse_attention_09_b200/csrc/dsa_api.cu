@@ -283,6 +283,7 @@ bool mla_shape_ok(int H, int k) { return H >= 1 && H <= 128 && k >= 64 && k <= 2
 
 // ---- row operators: norm, rotary positions, cache append ---------------------------------------
 constexpr int kSms = 148;
+constexpr int kMostCols = 1 << 30;  // columns of a row: the kernels' column numbers, a step past the row's end, fit an int
 
 bool dtype_ok(int32_t dtype) { return dtype == DSA_BF16 || dtype == DSA_F16 || dtype == DSA_F32; }
 size_t dtype_size(int32_t dtype) { return dtype == DSA_F32 ? 4 : 2; }
@@ -1070,7 +1071,7 @@ dsa_status dsa_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_
                    !same_rows(residual_out, ld_residual_out, residual, ld_residual)))
     return DSA_ERR_INVALID_ARGUMENT;
   if (y != nullptr && y == residual_out) return DSA_ERR_INVALID_ARGUMENT;
-  if (rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
+  if (rows > 0x7FFFFFFFLL || cols > kMostCols) return DSA_ERR_UNSUPPORTED;
   NormParams p;
   std::memset(&p, 0, sizeof(p));
   p.x = x;
@@ -1118,7 +1119,7 @@ dsa_status dsa_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, in
   if (ld_dy < 0 || ld_h < 0 || ld_dh < cols || (dresidual != nullptr && ld_dresidual < 0)) return DSA_ERR_INVALID_ARGUMENT;
   if (rows > 1 && (!same_rows(dh, ld_dh, dy, ld_dy) || !same_rows(dh, ld_dh, h, ld_h) || !same_rows(dh, ld_dh, dresidual, ld_dresidual)))
     return DSA_ERR_INVALID_ARGUMENT;
-  if (rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
+  if (rows > 0x7FFFFFFFLL || cols > kMostCols) return DSA_ERR_UNSUPPORTED;
   if (ws_bytes < dsa_rmsnorm_backward_workspace_size(rows, cols)) return DSA_ERR_WORKSPACE_TOO_SMALL;
   NormBwdParams p;
   std::memset(&p, 0, sizeof(p));
@@ -1163,7 +1164,7 @@ dsa_status dsa_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride, 
     return DSA_ERR_INVALID_ARGUMENT;
   if (out == x && ((rows > 1 && x_row_stride != out_row_stride) || (heads > 1 && x_head_stride != out_head_stride)))
     return DSA_ERR_INVALID_ARGUMENT;
-  if (rot_dim > 2 * rope::kMaxPairs || rows > 0x7FFFFFFFLL || static_cast<int64_t>(heads) * dim > 0x7FFFFFFFLL)
+  if (rot_dim > 2 * rope::kMaxPairs || rows > 0x7FFFFFFFLL || static_cast<int64_t>(heads) * dim > kMostCols)
     return DSA_ERR_UNSUPPORTED;
   RopeParams p;
   std::memset(&p, 0, sizeof(p));

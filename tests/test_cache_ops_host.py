@@ -262,3 +262,11 @@ def test_wrappers_take_a_head_dimension_of_one():
                           torch.zeros(2, dtype=torch.int32), 256)
     with pytest.raises(ValueError, match="current CUDA device"):  # refused for being on the CPU, not for its shape
         dsa.dsa_window_mla_decode(torch.zeros(2, 16, 576), desc, 2, 16, 8, 0, 0.04, torch.zeros(2, 16, 512))
+
+
+def test_rows_too_wide_for_32_bit_columns():
+    wide = 2 ** 31 - 512  # a step of 1024 past the last column leaves 32 bits
+    assert norm(cols=wide, ld_x=wide, ld_y=wide) == UNSUPPORTED
+    assert norm_bwd(cols=wide, ld_dy=wide, ld_h=wide, ld_dh=wide, size=1 << 62) == UNSUPPORTED
+    assert rope(heads=1, dim=wide, xr=wide, orow=wide) == UNSUPPORTED
+    assert rope(heads=2 ** 20, dim=2 ** 10 + 8, xh=2048, oh=2048, xr=2 ** 31, orow=2 ** 31) == UNSUPPORTED
