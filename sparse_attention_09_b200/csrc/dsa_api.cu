@@ -246,20 +246,21 @@ dsa_status launch_mla_pair(const void* latent, const void* q, int64_t q_rows, co
 // ---- window MLA --------------------------------------------------------------------------------
 // Whether decode shares the chunks of all sequences out over the clusters (and merges the split
 // sequences) instead of giving each cluster whole sequences.  In chunks' times: whole sequences take
-// rounds of (chunks + kUnitCost); shared, the even share, a quarter of it and 12 for what splits add (a
+// rounds of (chunks + kUnitCost); shared, the even share, an eighth of it and 8 for what splits add (a
 // second piece of work per cluster, fp32 partial outputs, the merge).  By the longest context the
 // arguments allow: the contexts themselves are on the device.
-// Measured (us, shared / whole): 8 sequences of 512 keys 20.6 / 19.6; 16 of 1024 27.5 / 27.8, of 2048
-// 31.8 / 45.9; of 4096 keys 48 sequences 82 / 85, 64: 103 / 90, 80: 125 / 163, 112: 177 / 165, 160: 235 / 247.
+// Measured (us, shared / whole): 8 sequences of 512 keys 16.0 / 16.1; of 1024 keys 8: 18.6 / 23.3, 24:
+// 24.8 / 23.7; of 2048 keys 16: 25 / 38, 40: 46 / 40, 96: 85 / 87; of 4096 keys 48: 78 / 81, 64: 101 / 87, 112: 162 / 178,
+// 128: 187 / 185; of 8192 keys 56: 149 / 182, 64: 189 / 180.
 constexpr int kShareSeqs = 1024;  // a cluster's start is found by a scan of the contexts
 
 bool window_shared(int B, int window, int sinks, int max_ctx) {
   const int64_t keys = std::min<int64_t>(max_ctx, static_cast<int64_t>(window) + sinks);
-  const int64_t chunks = (keys + 63) / 64;
+  const int64_t chunks = (keys + win::kChunk - 1) / win::kChunk;
   if (B > kShareSeqs || chunks < 2) return false;
   const int64_t whole = (B + kMlaClusters - 1) / kMlaClusters * (chunks + win::kUnitCost);
   const int64_t share = B * (chunks + win::kUnitCost) / kMlaClusters;
-  return share + share / 4 + 12 < whole;
+  return share + share / 8 + 8 < whole;
 }
 
 size_t window_plan_bytes(int B) { return align256(static_cast<size_t>(B) * sizeof(int2)); }

@@ -2,27 +2,38 @@
 //
 //   out[t,h,:] = sum_s softmax_s(sm_scale * q[t,h,:] . c_s) * c_s[0:512],  s <= t and (s > t - window or s < sinks)
 //
-// The two products, their split over the pair, the tiles and the TMEM columns are those of the sparse
-// kernel (sparse_mla_pair.cuh): CTA r owns heads [64r, 64r + 64); S = Q.K^T and O += P.V are pair MMAs
-// (M = 128) issued from CTA 0, K split by keys and V by value dims.  What differs:
+// The two products and their split over the pair are those of the sparse kernel (sparse_mla_pair.cuh):
+// CTA r owns heads [64r, 64r + 64); S = Q.K^T and O += P.V are pair MMAs (M = 128) issued from CTA 0, K
+// split by keys and V by value dims.  What differs:
 //   * the keys are not selected but numbered: entry e < ns is position e, entry e >= ns position
-//     e + (lo - ns), with lo = max(0, t + 1 - window) and ns = min(sinks, lo).  So every 64-key chunk but
-//     a query's last is full, nothing is masked but that chunk's tail (its logits are set to -inf in a
+//     e + (lo - ns), with lo = max(0, t + 1 - window) and ns = min(sinks, lo).  So every chunk but a
+//     query's last is full, nothing is masked but that chunk's tail (its logits are set to -inf in a
 //     branch of its own), and a row outside the window is never loaded: entries past the last are
 //     written as zeros, so that a NaN in an unused slot cannot reach P.V as 0 * NaN;
+//   * a chunk is 128 keys: Q.K^T with N = 128 reads Q from shared memory half as often per key as with
+//     64 (32 cycles of tensor work on 4 KB of operands, where N = 64 has 16 on 3 KB).  The room comes from
+//     staging one chunk of own rows by groups of 192 dims, each refilled as soon as its MMAs are done,
+//     and P and V by halves of 64 keys.  With 64-key chunks, two of them staged: 979 us against 871 on 3984
+//     tokens with a window of 1024, 2099 against 1833 on 5008 with 2048 (bursts), 90 against 80 for
+//     three decode sequences up to 128K; equal at windows of 128, and one key block of 64 or less costs
+//     1 % more in prefill, 1.3 us more (11.5) in a decode launch.  A last chunk of at most 64 keys
+//     has no second half: CTA r then stages keys [32r, 32r + 32) and the upper rows keep what they held,
+//     which reaches only columns of S that are masked;
 //   * the row sum is that of the unrounded fp32 probabilities (lse is an fp32 result of its own);
 //   * each issuing or relaying warp follows one stream of operands and waits for each barrier in turn;
 //   * a wait that runs out is remembered: the warp goes on without waiting (on whatever the buffers
 //     hold, all within them) and reports it at the end, so that no two warps have to agree on leaving;
 //   * decode: a cluster takes a share of all sequences' chunks (below).
 //
-// Bound: shared-memory bandwidth.  Per chunk and SM the MMAs read 156 KB (Q 72, K 36, P 16, V 32) and
-// the copies write 68 KB: 1.8K cycles at 128 B per cycle, against about 2K measured.
+// Bound: shared-memory bandwidth.  Per chunk and SM the MMAs read 240 KB (Q 72, K 72, P 32, V 64) and
+// the copies write 136 KB: 2.9K cycles at 128 B per cycle, against about 3.4K measured (2.2K of tensor work).
+// On 5008 tokens with a window of 2048: 1.83 to 1.91 ms in a burst (1.2 PFLOP/s), 2.12 to 2.16 under the power cap
+// (1.06, 0.77 of measured sustained bf16).
 // The instruction cache comes next: the roles' loops run side by side, and as a form of the sparse
-// kernel the same work took, on 5008 tokens with a window of 2048, 2.57 ms with that kernel's unstaged epilogue and 3.41
-// with the staged one inline in the softmax loop, against 2.16 ms here (1.05 PFLOP/s in a burst;
-// 2.47 ms, 0.92 PFLOP/s, 0.67 of measured sustained bf16, under the power cap), so loops are small and what is
-// rare is out of line.
+// kernel the same work (by 64 keys) took 2.57 ms with that kernel's unstaged epilogue and 3.41 with the staged
+// one inline in the softmax loop, against 2.16 ms on its own, so loops are small and what is rare is
+// out of line.  N of Q.K^T is the same for every chunk: chosen per chunk (64 for a last one
+// without a second half) the whole kernel took 2.01 ms instead of 1.91.
 #pragma once
 
 #include "common.cuh"
@@ -51,13 +62,10 @@ struct WinParams {
 
 namespace win {
 
-using mlap::kChunk;
 using mlap::kColO;
 using mlap::kColS;
 using mlap::kFirstProducerWarp;
 using mlap::kHeads;
-using mlap::kKQBlockBytes;
-using mlap::kKQBytes;
 using mlap::kMmaWarp;
 using mlap::kOffKQ;
 using mlap::kOffP;
@@ -76,19 +84,29 @@ using mlap::kVBlockBytes;
 using mlap::kVBytes;
 using mlap::kVWarp0;
 
+constexpr int kChunk = 128;                         // entries per pipeline step, in two halves of 64
+constexpr int kHalf = 64;
+constexpr int kKQBlockBytes = kHalf * 128;          // a CTA's 64 own rows x 64 dims
+constexpr int kGroups = 3;                          // own rows are staged by groups of 192 dims
+constexpr int kGroupBlocks = 3;
+constexpr int kGroupBytes = kGroupBlocks * kKQBlockBytes;
+static_assert(kOffKQ + kGroups * kGroupBytes == kOffV, "one chunk of own rows");
+
 // What a query costs beside its chunks (its Q, the pipeline's fill, the readout of O), in chunks:
-// measured 5 us against 1.3 to 1.5 per chunk.
-constexpr int kUnitCost = 4;
-// Decode: pages are brought into L2 this many chunks ahead of their copies (64 sequences, window 4096:
-// 94.1 us without, 87.8 / 88.1 / 92.7 us with 2 / 4 / 8).
-constexpr int kAhead = 4;
-constexpr int kMinShare = 2;  // chunks that a cluster takes at least when sequences are split
+// measured 3 to 4 us against 1.7 to 1.9 per chunk (1 and 3 share as evenly).
+constexpr int kUnitCost = 2;
+// Decode: pages are brought into L2 this many chunks ahead of their copies (one sequence of 128K 54.5 / 57.0 /
+// 62.6 us with 1 / 2 / 4, three up to 128K 78 / 79.5 / 88).
+constexpr int kAhead = 1;
+constexpr int kMinShare = 1;  // chunks that a cluster takes at least when sequences are split
 
 // The entries of a query that has `len` keys up to its own: entry e < ns is position e, a later one
 // below `end` position e + shift.
 struct Visible {
   int ns, shift, end;
   __device__ __forceinline__ int chunks() const { return max(1, (end - 1) / kChunk + 1); }  // 0 keys: one, masked whole
+  // Whether chunk c has keys in its second half; all but the last have.
+  __device__ __forceinline__ bool second(int c) const { return c * kChunk + kHalf < end; }
 };
 __device__ __forceinline__ Visible visible(const WinParams& p, int len) {
   len = max(len, 0);
@@ -345,14 +363,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(win::kThreads, 1)
   uint8_t* sV = smem + kOffV;
 
   // local to each CTA
-  __shared__ uint64_t bar_kq_full[2], bar_v_full[2];    // this CTA's rows of a slot have landed
-  __shared__ uint64_t bar_kq_empty[2], bar_v_empty[2];  // the MMAs reading a slot are done
+  __shared__ uint64_t bar_kq_full[kGroups], bar_v_full[2];  // this CTA's rows of a slot have landed
+  __shared__ uint64_t bar_kq_empty[kGroups];            // the MMAs reading a slot are done
   __shared__ uint64_t bar_q_full, bar_q_empty;          // Q staged / the piece's last Q.K^T done
-  __shared__ uint64_t bar_s_full[2], bar_pv_done[2];    // S of a slot written / P.V of a P slot done
+  __shared__ uint64_t bar_s_full[2], bar_pv_done[2];    // S of a slot written / P.V of a half done: its P and V slots are free
   __shared__ uint64_t bar_mma_done;                     // every MMA of the kernel has completed
   // used in CTA 0 only: arrivals from both CTAs, or of CTA 1's staged operands
-  __shared__ uint64_t bar_s_free[2], bar_p_full[2], bar_o_free;
-  __shared__ uint64_t bar_kq_peer[2], bar_v_peer[2], bar_q_peer;
+  __shared__ uint64_t bar_s_free[2], bar_p_full, bar_o_free;
+  __shared__ uint64_t bar_kq_peer[kGroups], bar_v_peer[2], bar_q_peer;
   __shared__ uint32_t s_tmem;
   __shared__ float s_red[3][2][kHeads];  // [buffer][key half][head] maxima / sums
   __shared__ Walk<DECODE> s_walk;
@@ -363,17 +381,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(win::kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar_kq_full[i], 64);  // every thread of the two gathering warps (plus its copies in flight)
-      mbar_init(&bar_v_full[i], 64);
-      mbar_init(&bar_kq_empty[i], 1);
-      mbar_init(&bar_v_empty[i], 1);
+      mbar_init(&bar_v_full[i], 64);  // every thread of the two gathering warps (plus its copies in flight)
       mbar_init(&bar_s_full[i], 1);
       mbar_init(&bar_pv_done[i], 1);
       mbar_init(&bar_s_free[i], 2 * kSoftmaxWarps);
-      mbar_init(&bar_p_full[i], 2 * kSoftmaxWarps);
-      mbar_init(&bar_kq_peer[i], 1);
       mbar_init(&bar_v_peer[i], 1);
     }
+    for (int i = 0; i < kGroups; ++i) {
+      mbar_init(&bar_kq_full[i], 64);
+      mbar_init(&bar_kq_empty[i], 1);
+      mbar_init(&bar_kq_peer[i], 1);
+    }
+    mbar_init(&bar_p_full, 2 * kSoftmaxWarps);
     mbar_init(&bar_q_full, 1);
     mbar_init(&bar_q_empty, 1);
     mbar_init(&bar_mma_done, 2);
@@ -418,8 +437,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(win::kThreads, 1)
   Work w;
 
   if (warp >= kFirstProducerWarp && warp < kFirstProducerWarp + 2) {
-    // ================= own rows, all 576 dims (B of Q.K^T): 16 of this CTA's 32 rows per warp =================
+    // ================= own rows, all 576 dims (B of Q.K^T): 32 of this CTA's 64 rows per warp =================
     const int pw = warp - kFirstProducerWarp;
+    const int ch = lane & 7;
     uint32_t g = 0;
     while (walk.next(p, cid, w)) {
       const int32_t* bt = DECODE ? p.block_table + static_cast<int64_t>(w.seq) * p.max_blocks : nullptr;
@@ -427,62 +447,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(win::kThreads, 1)
           (p.context_lens[w.seq] < 0 || p.context_lens[w.seq] > p.max_len))
         record_device_error(DSA_ERR_DEVICE_CHECK);  // the context is clamped
       for (int c = w.c0; c < w.c1; ++c, ++g) {
-        const int s = static_cast<int>(g & 1u);
+        const bool second = w.v.second(c);
+        const int own = second ? 32 : 16;  // rows of this warp
         bool bad;
-        const int row = row_of<DECODE>(p, bt, w, c * kChunk + 32 * static_cast<int>(rank) + 16 * pw + (lane & 15), bad);
-        if (bad && lane < 16) record_device_error(DSA_ERR_DEVICE_CHECK);  // the key is masked
+        const int row =
+            row_of<DECODE>(p, bt, w, c * kChunk + own * (2 * static_cast<int>(rank) + pw) + (lane & (own - 1)), bad);
+        if (bad && lane < own) record_device_error(DSA_ERR_DEVICE_CHECK);  // the key is masked
         if constexpr (DECODE) {
           // the page that the entries kAhead chunks ahead begin in, on its way from HBM in one instruction
-          const int e = (c + kAhead) * kChunk;
-          if (pw == 0 && lane == 0 && rank == (g & 1u) && c + kAhead < w.c1) {
+          const int e = (c + kAhead) * kChunk + kHalf * static_cast<int>(rank);
+          if (pw == 0 && lane == 0 && c + kAhead < w.c1 && e < w.v.end) {
             const int blk = bt[(e < w.v.ns ? e : e + w.v.shift) >> 6];
             if (blk >= 0 && blk < p.num_blocks) prefetch_page(latent + static_cast<int64_t>(blk) * 64 * 576);
           }
         }
-        wait(&bar_kq_empty[s], ((g >> 1) & 1u) ^ 1u);
-        const uint32_t kq = smem_addr(sKQ + s * kKQBytes);
-#pragma unroll 8
-        for (int j = 0; j < 16; ++j) {
-          const int r = 16 * pw + j;
-          const int kr = __shfl_sync(0xffffffffu, row, j);
-          const uint32_t dst = kq + (lane >> 3) * kKQBlockBytes + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
-          copy_piece(dst, latent, kr, 8 * lane);
-          copy_piece(dst + 4 * kKQBlockBytes, latent, kr, 256 + 8 * lane);
-        }
+#pragma unroll 1
+        for (int q = 0; q < kGroups; ++q) {
+          wait(&bar_kq_empty[q], (g & 1u) ^ 1u);
+          const uint32_t kq = smem_addr(sKQ + q * kGroupBytes) + own * pw * 128;
+          const int elem = 64 * kGroupBlocks * q + 8 * ch;
+#pragma unroll 1
+          for (int j0 = 0; j0 < own; j0 += 16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // rope dims 512-575: four rows per instruction
-          const int j = 4 * i + (lane >> 3), ch = lane & 7, r = 16 * pw + j;
-          const int kr = __shfl_sync(0xffffffffu, row, j);
-          copy_piece(kq + 8 * kKQBlockBytes + r * 128 + ((ch ^ (r & 7)) << 4), latent, kr, 512 + 8 * ch);
+            for (int i = 0; i < 4; ++i) {  // four rows' 128 bytes of a block per instruction
+              const int j = j0 + 4 * i + (lane >> 3);
+              const int kr = __shfl_sync(0xffffffffu, row, j);
+              const uint32_t dst = kq + j * 128 + ((ch ^ (j & 7)) << 4);
+#pragma unroll
+              for (int b = 0; b < kGroupBlocks; ++b) copy_piece(dst + b * kKQBlockBytes, latent, kr, elem + 64 * b);
+            }
+          }
+          cp_async_commit();
+          cp_async_mbar_arrive(&bar_kq_full[q]);
+          mbar_arrive(&bar_kq_full[q]);
         }
-        cp_async_commit();
-        cp_async_mbar_arrive(&bar_kq_full[s]);
-        mbar_arrive(&bar_kq_full[s]);
       }
     }
     cp_async_wait<0>();
   } else if (warp >= kVWarp0 && warp < kVWarp0 + 2) {
-    // ================= all 64 rows, this CTA's value dims (B of P.V): 32 rows per warp =================
+    // ================= all rows, this CTA's value dims (B of P.V): by halves, 32 rows per warp =================
     const int pw = warp - kVWarp0;
     const int seg = lane >> 4, pc = lane & 15;  // segment m: dims 256m + 128 rank + 8 pc
     const int ch = pc & 7, elem = 256 * seg + 128 * static_cast<int>(rank) + 8 * pc;
-    uint32_t g = 0;
+    uint32_t used[2] = {0, 0};
     while (walk.next(p, cid, w)) {
       const int32_t* bt = DECODE ? p.block_table + static_cast<int64_t>(w.seq) * p.max_blocks : nullptr;
-      for (int c = w.c0; c < w.c1; ++c, ++g) {
-        const int s = static_cast<int>(g & 1u);
-        bool bad;
-        const int row = row_of<DECODE>(p, bt, w, c * kChunk + 32 * pw + lane, bad);
-        wait(&bar_v_empty[s], ((g >> 1) & 1u) ^ 1u);
-        const uint32_t vb = smem_addr(sV + s * kVBytes) + (2 * seg + (pc >> 3)) * kVBlockBytes;
+      for (int c = w.c0; c < w.c1; ++c) {
+#pragma unroll 1
+        for (int s = 0; s <= (w.v.second(c) ? 1 : 0); ++s) {
+          bool bad;
+          const int row = row_of<DECODE>(p, bt, w, c * kChunk + kHalf * s + 32 * pw + lane, bad);
+          const uint32_t n_used = s == 0 ? used[0]++ : used[1]++;
+          wait(&bar_pv_done[s], (n_used & 1u) ^ 1u);
+          const uint32_t vb = smem_addr(sV + s * kVBytes) + (2 * seg + (pc >> 3)) * kVBlockBytes;
 #pragma unroll 8
-        for (int j = 0; j < 32; ++j) {
-          const int n = 32 * pw + j;
-          copy_piece(vb + n * 128 + ((ch ^ (n & 7)) << 4), latent, __shfl_sync(0xffffffffu, row, j), elem);
+          for (int j = 0; j < 32; ++j) {
+            const int n = 32 * pw + j;
+            copy_piece(vb + n * 128 + ((ch ^ (n & 7)) << 4), latent, __shfl_sync(0xffffffffu, row, j), elem);
+          }
+          cp_async_commit();
+          cp_async_mbar_arrive(&bar_v_full[s]);
+          mbar_arrive(&bar_v_full[s]);
         }
-        cp_async_commit();
-        cp_async_mbar_arrive(&bar_v_full[s]);
-        mbar_arrive(&bar_v_full[s]);
       }
     }
     cp_async_wait<0>();
@@ -509,31 +535,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(win::kThreads, 1)
     // the last load must have landed before the CTA may exit
     if (lane == 0 && tok > 0 && !mbar_wait(&bar_q_full, (tok - 1) & 1u)) ok = false;
   } else if (warp == kMmaWarp || warp == kPvWarp) {
-    uint32_t g = 0, tok = 0;
+    uint32_t g = 0, g1 = 0, tok = 0;  // chunks, chunks with a second half, pieces
     if (warp == kMmaWarp && rank == 0) {
       // ================= Q.K^T issuer (for the pair) =================
       const uint64_t ad = make_smem_desc(smem_addr(sQ), 16, 1024, kSwizzle128B);
+      const uint64_t bd = make_smem_desc(smem_addr(sKQ), 16, 1024, kSwizzle128B);
       while (walk.next(p, cid, w)) {
         wait(&bar_q_full, tok & 1u);
         wait(&bar_q_peer, tok & 1u);
         ++tok;
         for (int c = w.c0; c < w.c1; ++c, ++g) {
           const int s = static_cast<int>(g & 1u);
-          const uint32_t par = (g >> 1) & 1u;
-          wait(&bar_kq_full[s], par);
-          wait(&bar_kq_peer[s], par);
-          wait(&bar_s_free[s], par ^ 1u);
-          tc_fence_after();
-          if (lane == 0) fence_proxy_async_smem();  // the gathered rows were written through the generic proxy
-          __syncwarp();
-          const uint64_t bd = make_smem_desc(smem_addr(sKQ + s * kKQBytes), 16, 1024, kSwizzle128B);
+          wait(&bar_s_free[s], ((g >> 1) & 1u) ^ 1u);
+#pragma unroll 1
+          for (int q = 0; q < kGroups; ++q) {
+            wait(&bar_kq_full[q], g & 1u);
+            wait(&bar_kq_peer[q], g & 1u);
+            tc_fence_after();
+            if (lane == 0) fence_proxy_async_smem();  // the gathered rows were written through the generic proxy
+            __syncwarp();
+            const uint64_t aq = ad + ((q * kGroupBlocks * kQBlockBytes) >> 4), bq = bd + ((q * kGroupBytes) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 36; ++kk)
-            umma_bf16_ss_pair_warp(tmem + kColS + 32 * s, ad + (((kk >> 2) * kQBlockBytes + (kk & 3) * 32) >> 4),
-                                   bd + (((kk >> 2) * kKQBlockBytes + (kk & 3) * 32) >> 4), IDESC_QK, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < 4 * kGroupBlocks; ++kk)
+              umma_bf16_ss_pair_warp(tmem + kColS + 64 * s, aq + (((kk >> 2) * kQBlockBytes + (kk & 3) * 32) >> 4),
+                                     bq + (((kk >> 2) * kKQBlockBytes + (kk & 3) * 32) >> 4), IDESC_QK, q + kk > 0 ? 1u : 0u);
+            if (lane == 0) umma_commit_pair(&bar_kq_empty[q], 3);
+            __syncwarp();
+          }
           if (lane == 0) {
             umma_commit_pair(&bar_s_full[s], 3);
-            umma_commit_pair(&bar_kq_empty[s], 3);
             if (c == w.c1 - 1) umma_commit_pair(&bar_q_empty, 3);
           }
           __syncwarp();
@@ -547,11 +577,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(win::kThreads, 1)
         ++tok;
         if (lane == 0) mbar_arrive_peer(q_peer);
         for (int c = w.c0; c < w.c1; ++c, ++g) {
-          const uint32_t s = g & 1u;
-          wait(&bar_kq_full[s], (g >> 1) & 1u);
-          if (lane == 0) {
-            fence_proxy_async_smem();
-            mbar_arrive_peer(kq_peer + 8 * s);
+#pragma unroll 1
+          for (int q = 0; q < kGroups; ++q) {
+            wait(&bar_kq_full[q], g & 1u);
+            if (lane == 0) {
+              fence_proxy_async_smem();
+              mbar_arrive_peer(kq_peer + 8 * q);
+            }
           }
         }
       }
@@ -559,29 +591,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(win::kThreads, 1)
       // ================= P.V issuer (for the pair) =================
       while (walk.next(p, cid, w)) {
         for (int c = w.c0; c < w.c1; ++c, ++g) {
-          const int s = static_cast<int>(g & 1u);
-          const uint32_t par = (g >> 1) & 1u;
           const bool first = c == w.c0;
-          wait(&bar_v_full[s], par);
-          wait(&bar_v_peer[s], par);
           if (first) wait(&bar_o_free, (tok & 1u) ^ 1u);
-          wait(&bar_p_full[s], par);
-          tc_fence_after();
-          if (lane == 0) fence_proxy_async_smem();  // P (st.shared) and the value rows (cp.async): generic proxy
-          __syncwarp();
-          const uint64_t ad = make_smem_desc(smem_addr(sP + s * kPBytes), 16, 1024, kSwizzle128B);
-          const uint64_t bd = make_smem_desc(smem_addr(sV + s * kVBytes), kVBlockBytes, 1024, kSwizzle128B);
+          wait(&bar_p_full, g & 1u);
+#pragma unroll 1
+          for (int s = 0; s <= (w.v.second(c) ? 1 : 0); ++s) {
+            const uint32_t par = (s == 0 ? g : g1) & 1u;
+            wait(&bar_v_full[s], par);
+            wait(&bar_v_peer[s], par);
+            tc_fence_after();
+            if (lane == 0) fence_proxy_async_smem();  // P (st.shared) and the value rows (cp.async): generic proxy
+            __syncwarp();
+            const uint64_t ad = make_smem_desc(smem_addr(sP + s * kPBytes), 16, 1024, kSwizzle128B);
+            const uint64_t bd = make_smem_desc(smem_addr(sV + s * kVBytes), kVBlockBytes, 1024, kSwizzle128B);
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int kk = 0; kk < kChunk / 16; ++kk)
-              umma_bf16_ss_pair_warp(tmem + kColO + 128 * m, ad + ((kk * 32) >> 4),
-                                     bd + ((2 * m * kVBlockBytes + kk * 2048) >> 4), IDESC_PV, (first && kk == 0) ? 0u : 1u);
-          if (lane == 0) {
-            umma_commit_pair(&bar_pv_done[s], 3);
-            umma_commit_pair(&bar_v_empty[s], 3);
+              for (int kk = 0; kk < kHalf / 16; ++kk)
+                umma_bf16_ss_pair_warp(tmem + kColO + 128 * m, ad + ((kk * 32) >> 4),
+                                       bd + ((2 * m * kVBlockBytes + kk * 2048) >> 4), IDESC_PV,
+                                       (first && s + kk == 0) ? 0u : 1u);
+            if (lane == 0) umma_commit_pair(&bar_pv_done[s], 3);
+            __syncwarp();
+            if (s == 1) ++g1;
           }
-          __syncwarp();
         }
         ++tok;
       }
@@ -590,11 +623,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(win::kThreads, 1)
       const uint32_t v_peer = at_leader(&bar_v_peer[0]);
       while (walk.next(p, cid, w)) {
         for (int c = w.c0; c < w.c1; ++c, ++g) {
-          const uint32_t s = g & 1u;
-          wait(&bar_v_full[s], (g >> 1) & 1u);
-          if (lane == 0) {
-            fence_proxy_async_smem();
-            mbar_arrive_peer(v_peer + 8 * s);
+#pragma unroll 1
+          for (int s = 0; s <= (w.v.second(c) ? 1 : 0); ++s) {
+            wait(&bar_v_full[s], (s == 0 ? g : g1) & 1u);
+            if (s == 1) ++g1;
+            if (lane == 0) {
+              fence_proxy_async_smem();
+              mbar_arrive_peer(v_peer + 8 * s);
+            }
           }
         }
       }
@@ -613,43 +649,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(win::kThreads, 1)
     const int hl = 32 * (warp & 1) + lane;      // head row within the CTA (TMEM lane 32 warp + lane)
     const int h = kHeads * static_cast<int>(rank) + hl;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * warp) << 16);
-    const uint32_t s_free_l = at_leader(&bar_s_free[0]), p_full_l = at_leader(&bar_p_full[0]);
+    const uint32_t s_free_l = at_leader(&bar_s_free[0]), p_full_l = at_leader(&bar_p_full);
     const uint32_t o_free_l = at_leader(&bar_o_free);
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
-    uint32_t g = 0;
+    uint32_t g = 0, g1 = 0;  // chunks, chunks with a second half
     while (walk.next(p, cid, w)) {
       const int32_t* bt = DECODE ? p.block_table + static_cast<int64_t>(w.seq) * p.max_blocks : nullptr;
       float m = -INFINITY, l = 0.f;
       bool bad;
-      int row = row_of<DECODE>(p, bt, w, w.c0 * kChunk + 32 * kh + lane, bad);
+      bool second = w.v.second(w.c0);
+      int row[2];
+      // of chunk c: column i of this thread's S is key 64 kh + i, or 32 kh + i (i < 32) without a second half
+      auto rows_of = [&](int c, bool two) {
+        const int e = c * kChunk + (two ? kHalf : 32) * kh + lane;
+        row[0] = row_of<DECODE>(p, bt, w, e, bad);
+        row[1] = row_of<DECODE>(p, bt, w, two ? e + 32 : w.v.end, bad);
+      };
+      rows_of(w.c0, second);
       for (int c = w.c0; c < w.c1; ++c, ++g) {
         const int s = static_cast<int>(g & 1u);
-        const uint32_t vmask = __ballot_sync(0xffffffffu, row >= 0);
-        row = row_of<DECODE>(p, bt, w, (c + 1) * kChunk + 32 * kh + lane, bad);  // the next chunk's, ahead of its use
+        second = w.v.second(c);
+        const uint32_t vmask[2] = {__ballot_sync(0xffffffffu, row[0] >= 0), __ballot_sync(0xffffffffu, row[1] >= 0)};
+        rows_of(c + 1, w.v.second(c + 1));  // the next chunk's, ahead of its use
         wait(&bar_s_full[s], (g >> 1) & 1u);
         tc_fence_after();
-        uint32_t sr[32];
-        tmem_ld32(lane_base + kColS + 32 * s, sr);
+        uint32_t sr[2][32];
+        tmem_ld32(lane_base + kColS + 64 * s, sr[0]);
+        tmem_ld32(lane_base + kColS + 64 * s + 32, sr[1]);
         tmem_wait_ld();
-        reg_fence(sr);
+        reg_fence(sr[0]);
+        reg_fence(sr[1]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_peer(s_free_l + 8 * s);
         // only a query's last chunk (or a bad page) has masked keys: -inf, so that the maximum, the
         // exponentials and the sums need no masks
-        if (vmask != 0xffffffffu) {
+        if ((vmask[0] & vmask[1]) != 0xffffffffu) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((vmask >> i) & 1u)) sr[i] = 0xff800000u;
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((vmask[k] >> i) & 1u)) sr[k][i] = 0xff800000u;
         }
         // the row maximum over this half's keys, then with the partner half
         float mx[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(__uint_as_float(sr[j]), __uint_as_float(sr[j + 4]));
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(__uint_as_float(sr[0][j]), __uint_as_float(sr[0][j + 4]));
 #pragma unroll
-        for (int i = 8; i < 32; i += 8)
+        for (int i = 8; i < 64; i += 8)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(sr[i + j]), __uint_as_float(sr[i + j + 4]));
+          for (int j = 0; j < 4; ++j)
+            mx[j] = max3(mx[j], __uint_as_float(sr[i >> 5][(i & 31) + j]), __uint_as_float(sr[i >> 5][(i & 31) + j + 4]));
         const float hmax = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         s_red[s][kh][hl] = hmax;
         mlap::pair_sync(warp);
@@ -666,7 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(win::kThreads, 1)
         // tcgen05.ld/st are warp-collective: the whole warp runs the rescale if any row needs it
         // (the partner warp decides identically: same heads, same maxima)
         if (__any_sync(0xffffffffu, rescale)) {
-          wait(&bar_pv_done[(g - 1) & 1u], ((g - 1) >> 1) & 1u);
+          wait(&bar_pv_done[1], (g1 - 1) & 1u);  // the chunk before is whole
           tc_fence_after();
           rescale_o(lane_base + kColO, alpha);
           l *= alpha;
@@ -674,33 +724,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(win::kThreads, 1)
         const float neg_m = m == -INFINITY ? 0.f : -m;  // no key seen yet: -inf stays -inf
         const uint64_t neg_m2 = pack2(neg_m, neg_m);
         uint64_t sum2 = 0;
-        uint32_t pk[16];
+        uint32_t pk[32];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 x = unpack2(fma2(pack2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), scale2, neg_m2));
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t* e = &sr[i >> 4][2 * (i & 15)];
+          const float2 x = unpack2(fma2(pack2(__uint_as_float(e[0]), __uint_as_float(e[1])), scale2, neg_m2));
           const float a = mla::ex2_approx(x.x), b = mla::ex2_approx(x.y);
           pk[i] = pack_bf16x2(a, b);
           sum2 = add2(sum2, pack2(a, b));
         }
         const float2 sum = unpack2(sum2);
         l += sum.x + sum.y;
-        // P slot s is free once P.V of chunk g-2 has completed
-        wait(&bar_pv_done[s], ((g >> 1) & 1u) ^ 1u);
-        uint8_t* prow = sP + s * kPBytes + hl * 128;
+        // the P slot is free once its P.V of the chunk before has completed
+        const int slot = second ? kh : 0;
+        wait(&bar_pv_done[slot], ((slot == 0 ? g : g1) & 1u) ^ 1u);
+        uint8_t* prow = sP + slot * kPBytes + hl * 128;
+        const int x = (second ? 0 : 4 * kh) ^ (hl & 7);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(prow + (((4 * kh + i) ^ (hl & 7)) << 4)) =
-              make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        for (int i = 0; i < 8; ++i) {
+          if (i >= 4 && !second) break;
+          *reinterpret_cast<uint4*>(prow + ((i ^ x) << 4)) = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        }
         fence_proxy_async_smem();
+        if (second) ++g1;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_peer(p_full_l + 8 * s);
+        if (lane == 0) mbar_arrive_peer(p_full_l);
       }
       // ---- the piece's end: the row sum over both halves, then O ----
       s_red[2][kh][hl] = l;
       mlap::pair_sync(warp);
       const float lt = l + s_red[2][kh ^ 1][hl];
-      wait(&bar_pv_done[(g - 1) & 1u], ((g - 1) >> 1) & 1u);
+      wait(&bar_pv_done[second ? 1 : 0], ((second ? g1 : g) - 1) & 1u);
       tc_fence_after();
       uint8_t* stage = sP + kh * kPBytes + (warp & 1) * 4096;
       const int head0 = kHeads * static_cast<int>(rank) + 32 * (warp & 1);

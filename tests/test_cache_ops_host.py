@@ -166,15 +166,15 @@ def test_window_descriptor_refusals():
 
 
 def test_window_decode_workspace():
-    # chunks are shared out when the even share (a query counting 4 beside its own), a quarter of it and 12
-    # come to less than rounds of whole sequences over 74 clusters
+    # chunks of 128 keys are shared out when the even share (a query counting 2 beside its own), an eighth
+    # of it and 8 come to less than rounds of whole sequences over 74 clusters
     f = dsa.dsa_window_mla_workspace_size
     assert f(0, 128, 8, 0, 100) == 0 and f(4, 128, 0, 0, 100) == 0 and f(4, 128, 8, 0, 0) == 0
 
     def expected(B, H, window, sinks, ctx):
-        chunks = -(-min(ctx, window + sinks) // 64)
-        share = B * (chunks + 4) // 74
-        if B > 1024 or chunks < 2 or not share + share // 4 + 12 < -(-B // 74) * (chunks + 4):
+        chunks = -(-min(ctx, window + sinks) // 128)
+        share = B * (chunks + 2) // 74
+        if B > 1024 or chunks < 2 or not share + share // 8 + 8 < -(-B // 74) * (chunks + 2):
             return 0
         up = lambda n: -(-n // 256) * 256  # noqa: E731
         return up(B * 8) + up(148 * H * 512 * 4) + up(148 * H * 8)
