@@ -514,7 +514,8 @@ dsa_status dsa_cache_append(const void* kv, int64_t ld_kv, const void* kv_weight
  *     Calls that may overlap on the GPU need workspaces of their own.  Keys in blocks outside the pool are masked and set DSA_ERR_DEVICE_CHECK.
  * Forward only, like every attention of this library.  1 <= H <= 128 (64-head tiles: small H costs as
  * much as 128).  DSA_ERR_INVALID_ARGUMENT: as dsa_sparse_mla_*, window < 1, sinks < 0, sm_scale not
- * positive and finite; DSA_ERR_UNSUPPORTED: H, the page size, or sizes beyond 2^31 - 1 rows.
+ * positive and finite; DSA_ERR_UNSUPPORTED: H, the page size, sizes beyond 2^31 - 1
+ * rows, or in decode max_seqlen > 2^30.
  */
 dsa_status dsa_window_mla_prefill(const void* q, const dsa_kv_desc* latent, int32_t B, int32_t H, int32_t window,
                                   int32_t sinks, float sm_scale, void* out, float* lse, void* stream);

@@ -1338,6 +1338,7 @@ dsa_status dsa_window_mla_decode(const void* q, const dsa_kv_desc* latent, int32
     return DSA_ERR_INVALID_ARGUMENT;
   if (static_cast<int64_t>(latent->num_blocks) * 64 > 0x7FFFFFFFLL || static_cast<int64_t>(B) * H > 0x7FFFFFFFLL - 128)
     return DSA_ERR_UNSUPPORTED;
+  if (latent->max_seqlen > 1 << 30) return DSA_ERR_UNSUPPORTED;  // entry numbers, a chunk past the last, fit an int
   p.shared = window_shared(B, window, sinks, latent->max_seqlen);
   if (p.shared) {
     if (workspace == nullptr || !aligned(workspace, 256)) return DSA_ERR_INVALID_ARGUMENT;

@@ -270,3 +270,7 @@ def test_rows_too_wide_for_32_bit_columns():
     assert norm_bwd(cols=wide, ld_dy=wide, ld_h=wide, ld_dh=wide, size=1 << 62) == UNSUPPORTED
     assert rope(heads=1, dim=wide, xr=wide, orow=wide) == UNSUPPORTED
     assert rope(heads=2 ** 20, dim=2 ** 10 + 8, xh=2048, oh=2048, xr=2 ** 31, orow=2 ** 31) == UNSUPPORTED
+
+
+def test_contexts_too_long_for_32_bit_entries():
+    assert window_decode(paged(max_seqlen=2 ** 30 + 1, per=2 ** 25)) == UNSUPPORTED
