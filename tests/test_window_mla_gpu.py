@@ -321,3 +321,19 @@ def test_wrapper_refusals():
     with pytest.raises(ValueError):
         dsa.dsa_window_mla_prefill(q, flat, 1, 128, 10, 0, SM, out)  # as many queries as tokens
     assert (out == 0).all()
+
+
+@pytest.mark.parametrize("sinks", [0, 3, 64])
+def test_decode_of_every_last_chunk(sinks):
+    """Key counts on either side of the halves and the wholes of a chunk, whole sequences and shared out."""
+    counts = [n + d for n in (64, 128, 192, 256) for d in (-1, 0, 1)] + [31, 32, 33]
+    ctx = counts + [c + 1000 for c in counts]
+    latent, table, logical = paged_cache(ctx)
+    table = torch.nn.functional.pad(table, (0, 141 - table.shape[1]), value=-1).contiguous()
+    q = rnd((len(ctx), 16, 576), 5, 2.0)
+    for window, shared in [(1 << 20, True)] + [(c, False) for c in (32, 63, 64, 65, 127, 128, 129, 191, 193, 256)]:
+        assert (dsa.dsa_window_mla_workspace_size(len(ctx), 16, window, sinks, 9000) > 0) == shared
+        out, lse = decode_call(q, latent, table, ctx, window, sinks, H=16, max_ctx=9000)
+        assert dsa.dsa_device_error() == 0
+        for b, c in enumerate(ctx):
+            check_row(f64(out[b]), f64(lse[b]), f64(q[b]), f64(logical[b]), c, window, sinks, (window, b))
