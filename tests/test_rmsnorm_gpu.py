@@ -189,7 +189,7 @@ def test_backward(cols, dtype):
         check_backward(dy, h, w, rstd, dres, *backward(dy, h, w, rstd, dres))
 
 
-@pytest.mark.parametrize("rows,cols", [(4000, 128), (1500, 2048), (1300, 1001), (5000, 8)])
+@pytest.mark.parametrize("rows,cols", [(4000, 128), (1500, 2048), (1300, 1001), (5000, 8), (6000, 131), (5000, 202), (5000, 252)])
 def test_backward_over_many_rows_repeats_its_bits(rows, cols):
     dy, h, w = rnd((rows, cols), torch.bfloat16, 1), rnd((rows, cols), torch.bfloat16, 2), rnd((cols,), torch.bfloat16, 3)
     rstd = (h.double().square().mean(1) + EPS).rsqrt().float()
