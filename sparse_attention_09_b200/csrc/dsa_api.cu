@@ -331,16 +331,19 @@ dsa_status launch_rmsnorm_v(const NormParams& p, cudaStream_t s) {
   return launch_status();
 }
 
-// Pieces of 4, 2 or 1 elements.
+// Pieces of 4, 2 or 1 elements.  Up to 512 columns a warp per row, beyond that a CTA with 16 elements per
+// thread (bf16, CTA against warp: 65536 x 1001 64.5 us against 70.4, x 1004 67 against 88; with residual and codes
+// 172 against 242; but x 500 45 against 37.  8 per thread: 20000 x 3001 72 against 64, x 7004 337 against 189).  Few
+// rows whose codes wait for a group's maximum: 8 elements per thread (64 x 501 with codes by groups 3.1 us against
+// 4.7 with a warp, x 3001 3.8 against 4.7 with 16).
 template <typename T, int V>
 dsa_status launch_rmsnorm_small(const NormParams& p, cudaStream_t s) {
   constexpr int kMin = V == 4 ? 1 : 4 / V;  // pieces per lane that make whole groups of 128 columns
   if (p.cols <= 128) return launch_rmsnorm_v<T, V, kMin, 32>(p, s);
   if (p.cols <= 256) return launch_rmsnorm_v<T, V, 2 * kMin, 32>(p, s);
+  if (p.codes != nullptr && p.rows <= 4 * kSms && p.cols <= 8192) return launch_rmsnorm_v<T, V, 2 * kMin, 0>(p, s);
   if (p.cols <= 512) return launch_rmsnorm_v<T, V, 4 * kMin, 32>(p, s);
-  if (p.cols <= 1024) return launch_rmsnorm_v<T, V, 8 * kMin, 32>(p, s);
-  if (p.cols <= 2048 * V * kMin) return launch_rmsnorm_v<T, V, 2 * kMin, 0>(p, s);
-  if (p.cols <= 4096 * V * kMin) return launch_rmsnorm_v<T, V, 4 * kMin, 0>(p, s);
+  if (p.cols <= 16384) return launch_rmsnorm_v<T, V, 4 * kMin, 0>(p, s);
   rmsnorm_general_kernel<T><<<static_cast<unsigned>(p.rows), norm::kGeneralThreads, 0, s>>>(p);
   return launch_status();
 }

@@ -96,6 +96,14 @@ def test_forward_many_rows_and_wide_ones(rows, cols):
     check_forward(x, w, res, "group", forward(x, w, res, "group"))
 
 
+@pytest.mark.parametrize("cols", [130, 251, 258, 500, 501, 513, 516, 777, 1001, 1002, 2052, 3001])
+@pytest.mark.parametrize("quant", ["row", "group"])
+def test_small_pieces_of_few_and_many_rows(cols, quant):
+    for rows in (5, 593):
+        x, w, res = rnd((rows, cols), torch.bfloat16, 1), 1 + rnd((cols,), torch.bfloat16, 2, 0.1), rnd((rows, cols), torch.bfloat16, 3)
+        check_forward(x, w, res, quant, forward(x, w, res, quant))
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("offset,stride", [(0, 520), (8, 1024), (3, 517), (0, 515)])
 def test_strided_and_misaligned_rows(dtype, offset, stride):
