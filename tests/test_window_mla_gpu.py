@@ -337,3 +337,30 @@ def test_decode_of_every_last_chunk(sinks):
         assert dsa.dsa_device_error() == 0
         for b, c in enumerate(ctx):
             check_row(f64(out[b]), f64(lse[b]), f64(q[b]), f64(logical[b]), c, window, sinks, (window, b))
+
+
+def test_two_captured_graphs_in_turn_over_one_workspace():
+    """Replayed one after the other, with the contexts changed between them; each replay plans and merges anew."""
+    H, window = 16, 1 << 20
+    latent, table, logical = paged_cache([3000, 900, 2000])
+    qs = [rnd((3, H, 576), s, 2.0) for s in (5, 6)]
+    ctx = torch.tensor([3000, 900, 2000], dtype=torch.int32, device="cuda")
+    desc = dsa.paged_desc(latent, table, ctx, 3000)
+    ws = torch.full((dsa.dsa_window_mla_workspace_size(3, H, window, 0, 3000),), 0xFF, dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
+    outs, lses, graphs = [torch.empty(3, H, 512, dtype=torch.bfloat16, device="cuda") for _ in qs], [torch.empty(3, H, device="cuda") for _ in qs], []
+    for q, out, lse in zip(qs, outs, lses):
+        dsa.dsa_window_mla_decode(q, desc, 3, H, window, 0, SM, out, lse, ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            dsa.dsa_window_mla_decode(q, desc, 3, H, window, 0, SM, out, lse, ws)
+    for lens in ([3000, 900, 2000], [64, 1, 1999], [0, 900, 129]):
+        ctx.copy_(torch.tensor(lens, dtype=torch.int32))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for q, out, lse in zip(qs, outs, lses):
+            for b, c in enumerate(lens):
+                check_row(f64(out[b]), f64(lse[b]), f64(q[b]), f64(logical[b]), c, window, 0, (lens, b))
+    assert dsa.dsa_device_error() == 0
