@@ -7,8 +7,8 @@
 // unrounded, and the 8-bit codes come from the unrounded v).
 //
 // HBM-bound: a row is read once and kept in registers (as fp32 h) between the sum of squares, the
-// maximum of its codes and the writes.  A row belongs to one CTA, or, up to 1024 columns, to one
-// warp or a half or quarter of one (no block barrier).  Rows that are not made of aligned pieces of 8
+// maximum of its codes and the writes.  A row belongs to one CTA, or, up to 1024 columns (512 in
+// pieces smaller than 8), to one warp or a half or quarter of one (no block barrier).  Rows that are not made of aligned pieces of 8
 // elements use the same kernels with pieces of 4, 2 or 1.  Rows too wide for the registers of a CTA take
 // the general kernels, which read a row again for each pass (from L1 / L2).
 // Measured on 32768 x 4096 bf16 with residual, y and codes: 180 us (6.7 TB/s, 1.02 of measured HBM's copy
