@@ -395,8 +395,8 @@ typedef enum { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_NTK = 2, DSA_RO
  *   rs = 1 / sqrt(mean(h^2) + eps),  v = h * rs * weight
  *   residual_out[r,:] = h          (when not NULL)
  *   y[r,:] = v                     (when not NULL)
- *   codes[r*cols + c] = e4m3(v_c / s), s = amax |v| / 448 (1 where the maximum is 0; the quotient
- *     formed as v_c * (1 / s)), over the row
+ *   codes[r*cols + c] = e4m3(v_c / s), s = amax |v| / 448 (at least 2^-149, the smallest fp32, where
+ *     the maximum is not 0; 1 where it is; the quotient formed as v_c * (1 / s)), over the row
  *     (group = 0: scale [rows]) or over each DSA_QUANT_GROUP columns (group = DSA_QUANT_GROUP:
  *     scale [rows, ceil(cols / 128)]), taken from the unrounded v, saturating at +-448.  NaN takes
  *     no part in the maximum and encodes as NaN.  codes and scale come together (both or neither).
@@ -476,8 +476,8 @@ dsa_status dsa_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling, 
  *   latent row: kv[r, 0:512] RMS-normalised with kv_weight [512] and eps, kv[r, 512:576] rotated
  *     (dsa_rope with `layout`), both in fp32, rounded once to bf16;
  *   indexer key: key[r, :] with dims [key_rot_offset, key_rot_offset + 64) rotated (`key_layout`),
- *     quantised to e4m3 as dsa_rmsnorm does a row (scale = amax / 448 from the unrounded values, 1 for
- *     an all-zero row).
+ *     quantised to e4m3 as dsa_rmsnorm does a row (scale = amax / 448 from the unrounded values, at least
+ *     2^-149; 1 for an all-zero row).
  * kv [rows, 576] and key [rows, d_I] are bf16 with row strides ld_*; freqs [32] fp64 (device).
  * latent and keys describe the caches (contiguous or paged; the library writes data and scale):
  * paged, position p of sequence b is row block_table[b, p/64] * 64 + p % 64; contiguous, row

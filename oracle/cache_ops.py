@@ -21,13 +21,14 @@ def rmsnorm(x, weight, eps, residual=None):
 
 
 def row_scales(v, group=0):
-    """amax / 448 over each row (group 0) or each `group` columns of it; 1 where the maximum is 0."""
+    """amax / 448, at least the smallest fp32, over each row (group 0) or each `group` columns of it; 1 where the
+    maximum is 0."""
     v = np.abs(np.asarray(v, np.float64))
     if group:
         amax = np.stack([v[:, c:c + group].max(axis=1) for c in range(0, v.shape[1], group)], axis=1)
     else:
         amax = v.max(axis=1)
-    return np.where(amax > 0, amax / E4M3_MAX, 1.0)
+    return np.where(amax > 0, np.maximum(amax / E4M3_MAX, 2.0 ** -149), 1.0)
 
 
 def rmsnorm_backward(dy, h, weight, rstd, dresidual=None):

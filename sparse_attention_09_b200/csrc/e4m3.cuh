@@ -6,8 +6,12 @@
 namespace dsa {
 namespace quant {
 
+// The smallest scale.  amax / 448 rounds to 0 below 448 * 2^-150, and 0 / 0 would be a NaN code; over this
+// scale such values (multiples of 2^-149) are exact quotients of at most 224.
+constexpr float kLeastScale = 0x1p-149f;
+
 // The scale of values with this largest magnitude (1 for none).
-__device__ __forceinline__ float scale_of(float amax) { return amax > 0.f ? __fdiv_rn(amax, kE4m3Max) : 1.f; }
+__device__ __forceinline__ float scale_of(float amax) { return amax > 0.f ? fmaxf(__fdiv_rn(amax, kE4m3Max), kLeastScale) : 1.f; }
 
 // 1 / s for over(), or 0 where s is so small that 1 / s could overflow.
 __device__ __forceinline__ float inverse_of(float s) { return s > 0x1p-120f ? __fdiv_rn(1.f, s) : 0.f; }

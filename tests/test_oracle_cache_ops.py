@@ -120,3 +120,10 @@ def test_window_attention_against_the_library_under_a_mask(length, window, sinks
     assert np.allclose(out, ref[:, 0].numpy(), atol=1e-12)
     logits = 0.05 * q @ lat[mask.numpy()].T
     assert np.allclose(lse, np.log(np.exp(logits).sum(1)))
+
+
+def test_row_scales_stop_at_the_smallest_fp32():
+    v = np.zeros((2, 130))
+    v[0, 0], v[0, 129], v[1, 0] = 448.0, 1.3e-43, 1e-40
+    assert oracle.row_scales(v).tolist() == [1.0, 1e-40 / 448]
+    assert oracle.row_scales(v, 128).tolist() == [[1.0, 2.0 ** -149], [1e-40 / 448, 1.0]]
