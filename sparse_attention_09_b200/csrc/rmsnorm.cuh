@@ -18,6 +18,7 @@
 
 #include "elem.cuh"
 #include "e4m3.cuh"
+#include "ring.cuh"
 
 namespace dsa {
 
@@ -468,6 +469,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_ring_kernel(const NormB
   const float inv_cols = 1.f / static_cast<float>(p.cols);
   __syncthreads();
   bool ok = true;  // a copy that does not land within the limit is reported, and not waited for again
+  int landed = 0;  // rows whose copies this thread has seen land
   int s = 0;
   uint32_t phase = 0;
   int it = 0;
@@ -476,6 +478,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_ring_kernel(const NormB
     const float rs = next_rs;
     if (row + gridDim.x < p.rows) next_rs = p.rstd[row + gridDim.x];
     if (ok) ok = dev::mbar_wait(&full[s], phase);
+    if (ok) ++landed;
     const uint8_t* src = ring + s * stage_bytes;
     Raw8<T> a, b, d;
     a.zero();
@@ -519,9 +522,13 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_ring_kernel(const NormB
   }
   if (!ok) {
     record_device_error(DSA_ERR_TIMEOUT);
-    // copies still in flight must not outlive the CTA's shared memory
-    if (t == 0)
-      for (int i = 0; i < stages; ++i) dev::mbar_wait(&full[i], phase);
+    // copies still in flight must not outlive the CTA's shared memory.  Thread 0 issues them, and issues none
+    // once its own wait has run out; when only another thread's has, it has seen them all land.
+    if (t == 0) {
+      const int copies = static_cast<int>((p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);  // the CTA's rows
+      for (int n = landed; n < ring_end(landed, stages, copies); ++n)
+        dev::mbar_wait(&full[ring_stage(n, stages)], ring_parity(n, stages));
+    }
   }
   if (in) {
     float4* part = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(blockIdx.x) * p.cols + c);
