@@ -426,7 +426,7 @@ dsa_status dsa_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_
  * dw is summed in a fixed order (a run repeats its bits).  dh may be dy or dresidual itself
  * (same pointer and stride).
  * workspace (device, 16-byte aligned): dsa_rmsnorm_backward_workspace_size(rows, cols) bytes, else
- * DSA_ERR_WORKSPACE_TOO_SMALL.  rows == 0 sets dw to zero.  Other errors as dsa_rmsnorm.
+ * DSA_ERR_WORKSPACE_TOO_SMALL; what suffices for these sizes suffices for fewer rows and narrower ones.  rows == 0 sets dw to zero.  Other errors as dsa_rmsnorm.
  */
 dsa_status dsa_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* weight,
                                 const float* rstd, const void* dresidual, int64_t ld_dresidual, int64_t rows,

@@ -1106,7 +1106,14 @@ dsa_status dsa_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_
 
 size_t dsa_rmsnorm_backward_workspace_size(int64_t rows, int32_t cols) {
   if (rows <= 0 || cols <= 0) return 0;
-  return align256(static_cast<size_t>(norm_bwd_ctas(rows, cols, 2)) * cols * sizeof(float));
+  // The CTAs fall as rows widen, so a narrower row can need more: the most of all widths up to cols.  Those with
+  // k CTAs per SM reach to 8192 / k columns (norm_bwd_per_sm at 2 bytes); with one there is no limit.
+  int64_t most = norm_bwd_ctas(rows, cols, 2) * cols;
+  for (int k = 2; k <= 16; ++k) {
+    const int widest = std::min(cols, 8192 / k);
+    most = std::max(most, norm_bwd_ctas(rows, widest, 2) * widest);
+  }
+  return align256(static_cast<size_t>(most) * sizeof(float));
 }
 
 dsa_status dsa_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* weight,

@@ -274,3 +274,19 @@ def test_rows_too_wide_for_32_bit_columns():
 
 def test_contexts_too_long_for_32_bit_entries():
     assert window_decode(paged(max_seqlen=2 ** 30 + 1, per=2 ** 25)) == UNSUPPORTED
+
+
+def test_rmsnorm_backward_workspace_serves_smaller_calls():
+    """One workspace for the widest layer and the longest batch serves all others; without the rule 65536 rows of 5120 columns
+    asked for 3.03 MB and of 4096 columns for 4.85 MB."""
+    f = dsa.dsa_rmsnorm_backward_workspace_size
+    for rows in (1, 37, 148, 149, 1000, 2367, 2368, 65536):
+        sizes = [f(rows, c) for c in range(1, 12300)]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])), rows
+        # what a call of these sizes writes: a row of partial sums for each of min(rows, 148 x (16 KB / row, 1 to 16)) CTAs
+        own = [min(rows, 148 * min(max(16384 // (2 * c), 1), 16)) * c * 4 for c in range(1, 12300)]
+        most = np.maximum.accumulate(own)
+        assert all(s == -(-int(m) // 256) * 256 for s, m in zip(sizes, most)), rows
+    for cols in (8, 500, 4096, 5120, 20000):
+        sizes = [f(r, cols) for r in list(range(1, 2500)) + [10 ** 6, 2 ** 31 - 1]]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])), cols
