@@ -510,7 +510,8 @@ dsa_status dsa_cache_append(const void* kv, int64_t ld_kv, const void* kv_weight
  *     to [0, latent->max_seqlen] (clamping sets DSA_ERR_DEVICE_CHECK).  When the sequences
  *     alone do not fill the GPU evenly, the chunks of all of them are shared out over it, whatever
  *     their lengths; the parts of split sequences go to `workspace` (256-byte aligned,
- *     dsa_window_mla_workspace_size bytes; may be NULL where that is 0) and are merged by log-sum-exp.
+ *     dsa_window_mla_workspace_size bytes; may be NULL where that is 0; for batches that change in
+ *     size dsa_window_mla_workspace_limit) and are merged by log-sum-exp.
  *     Calls that may overlap on the GPU need workspaces of their own.  Keys in blocks outside the pool are masked and set DSA_ERR_DEVICE_CHECK.
  * Forward only, like every attention of this library.  1 <= H <= 128 (64-head tiles: small H costs as
  * much as 128).  DSA_ERR_INVALID_ARGUMENT: as dsa_sparse_mla_*, window < 1, sinks < 0, sm_scale not
@@ -522,9 +523,12 @@ dsa_status dsa_window_mla_prefill(const void* q, const dsa_kv_desc* latent, int3
 dsa_status dsa_window_mla_decode(const void* q, const dsa_kv_desc* latent, int32_t B, int32_t H, int32_t window,
                                  int32_t sinks, float sm_scale, void* out, float* lse, void* workspace,
                                  size_t ws_bytes, void* stream);
-/* Workspace bytes of dsa_window_mla_decode (max_ctx = latent->max_seqlen; 0 when each sequence is
- * worked on whole). */
+/* Workspace bytes of dsa_window_mla_decode for one call (max_ctx = latent->max_seqlen; 0 when each
+ * sequence is worked on whole).  Not monotone: with a window of 4096, 64 sequences need none, 48 some 39 MB. */
 size_t dsa_window_mla_workspace_size(int32_t B, int32_t H, int32_t window, int32_t sinks, int32_t max_ctx);
+/* Workspace bytes that serve every call with at most these sequences, heads, window, sinks and
+ * max_seqlen: what a program keeps whose batch shrinks and grows. */
+size_t dsa_window_mla_workspace_limit(int32_t B, int32_t H, int32_t window, int32_t sinks, int32_t max_ctx);
 
 #ifdef __cplusplus
 }

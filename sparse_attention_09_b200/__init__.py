@@ -51,7 +51,7 @@ EXPORTED = ("dsa_indexer_scores", "dsa_indexer_topk", "dsa_topk", "dsa_sparse_ml
             "dsa_decode_select_workspace_size", "dsa_attn_distribution_dense", "dsa_indexer_backward",
             "dsa_rmsnorm", "dsa_rmsnorm_backward", "dsa_rmsnorm_backward_workspace_size", "dsa_rope",
             "dsa_rope_frequencies", "dsa_cache_append", "dsa_window_mla_prefill", "dsa_window_mla_decode",
-            "dsa_window_mla_workspace_size")
+            "dsa_window_mla_workspace_size", "dsa_window_mla_workspace_limit")
 
 
 class KVDesc(ctypes.Structure):
@@ -143,6 +143,8 @@ _lib.dsa_window_mla_decode.argtypes = [_P, _DESC, _I32, _I32, _I32, _I32, _F32, 
 _lib.dsa_window_mla_decode.restype = _I32
 _lib.dsa_window_mla_workspace_size.argtypes = [_I32, _I32, _I32, _I32, _I32]
 _lib.dsa_window_mla_workspace_size.restype = _SZ
+_lib.dsa_window_mla_workspace_limit.argtypes = [_I32, _I32, _I32, _I32, _I32]
+_lib.dsa_window_mla_workspace_limit.restype = _SZ
 
 
 class DSAError(RuntimeError):
@@ -489,12 +491,18 @@ def dsa_window_mla_prefill(q, latent: Desc, B, H, window, sinks, sm_scale, out, 
 
 
 def dsa_window_mla_workspace_size(B, H, window, sinks, max_ctx) -> int:
+    """Bytes for one dsa_window_mla_decode call; a smaller batch can need more (see dsa_window_mla_workspace_limit)."""
     return int(_lib.dsa_window_mla_workspace_size(int(B), int(H), int(window), int(sinks), int(max_ctx)))
+
+
+def dsa_window_mla_workspace_limit(B, H, window, sinks, max_ctx) -> int:
+    """Bytes for every dsa_window_mla_decode call with at most these sequences, heads, window, sinks and context."""
+    return int(_lib.dsa_window_mla_workspace_limit(int(B), int(H), int(window), int(sinks), int(max_ctx)))
 
 
 def dsa_window_mla_decode(q, latent: Desc, B, H, window, sinks, sm_scale, out, lse=None, workspace=None, stream=None):
     """The same for one query per sequence at position ctx - 1 over the paged latent cache;
-    workspace: dsa_window_mla_workspace_size bytes (None where that is 0)."""
+    workspace: dsa_window_mla_workspace_size bytes (None where that is 0), or _limit's for batches that change in size."""
     w = "dsa_window_mla_decode"
     _check(_marshal.window_decode(q, _windowed(w, q, latent, B), B, H, window, sinks, sm_scale, out, lse, workspace,
                                   _handle(stream)), w)

@@ -1331,10 +1331,21 @@ dsa_status dsa_window_mla_prefill(const void* q, const dsa_kv_desc* latent, int3
   return launch_window<false>(latent->data, q, p, p.rows, as_stream(stream));
 }
 
+static size_t window_workspace_bytes(int32_t B, int32_t H) {
+  return window_plan_bytes(B) + window_part_bytes(H) + align256(static_cast<size_t>(2 * kMlaClusters) * H * 2 * 4);
+}
+
 size_t dsa_window_mla_workspace_size(int32_t B, int32_t H, int32_t window, int32_t sinks, int32_t max_ctx) {
   if (B <= 0 || H <= 0 || window < 1 || sinks < 0 || max_ctx <= 0) return 0;
-  if (!window_shared(B, window, sinks, max_ctx)) return 0;
-  return window_plan_bytes(B) + window_part_bytes(H) + align256(static_cast<size_t>(2 * kMlaClusters) * H * 2 * 4);
+  return window_shared(B, window, sinks, max_ctx) ? window_workspace_bytes(B, H) : 0;
+}
+
+size_t dsa_window_mla_workspace_limit(int32_t B, int32_t H, int32_t window, int32_t sinks, int32_t max_ctx) {
+  if (B <= 0 || H <= 0 || window < 1 || sinks < 0 || max_ctx <= 0) return 0;
+  // One sequence is shared out as soon as any number of them is: that takes whole - share > 8, and whole - share is
+  // below (chunks + 2) (rounds - B / 74) + 1 <= (chunks + 2) 73 / 74 + 1, which leaves chunks >= 7, where one is.
+  if (!window_shared(1, window, sinks, max_ctx)) return 0;
+  return window_workspace_bytes(std::min(B, kShareSeqs), H);
 }
 
 dsa_status dsa_window_mla_decode(const void* q, const dsa_kv_desc* latent, int32_t B, int32_t H, int32_t window,

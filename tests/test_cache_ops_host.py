@@ -290,3 +290,24 @@ def test_rmsnorm_backward_workspace_serves_smaller_calls():
     for cols in (8, 500, 4096, 5120, 20000):
         sizes = [f(r, cols) for r in list(range(1, 2500)) + [10 ** 6, 2 ** 31 - 1]]
         assert all(a <= b for a, b in zip(sizes, sizes[1:])), cols
+
+
+def test_window_workspace_limit_serves_smaller_batches():
+    """The need of one call is not monotone (64 sequences none, 48 some); the limit covers every smaller call and is reached."""
+    size, limit = dsa.dsa_window_mla_workspace_size, dsa.dsa_window_mla_workspace_limit
+    assert size(64, 128, 4096, 16, 32768) == 0 and size(48, 128, 4096, 16, 32768) > 0
+    assert limit(0, 128, 8, 0, 100) == 0 and limit(4, 128, 0, 0, 100) == 0 and limit(4, 0, 8, 0, 100) == 0 and limit(4, 128, 8, -1, 9) == 0
+    for keys in list(range(1, 2000, 63)) + [767, 768, 769, 896, 897, 4112, 32768, 131072]:
+        most, smaller = 0, limit(1, 128, keys, 0, 2 ** 30)
+        for B in range(1, 1200):
+            most = max(most, size(B, 128, keys, 0, 2 ** 30), size(B, 128, 2 ** 30, 0, keys))
+            got = limit(B, 128, keys, 0, 2 ** 30)
+            assert got == limit(B, 128, 2 ** 30, 5, keys) >= max(most, smaller) and (got == 0) == (most == 0), (B, keys)
+            assert got - most <= B * 8 + 256  # the plan of the largest batch beside the parts of another
+            smaller = got
+        assert limit(64, 64, keys, 0, 2 ** 30) <= limit(64, 128, keys, 0, 2 ** 30) <= limit(64, 128, keys + 1, 0, 2 ** 30)
+    d = paged(max_seqlen=32768, per=512)
+    need = limit(64, 128, 4096, 16, 32768)
+    for B in (1, 2, 40, 48):
+        assert 0 < size(B, 128, 4096, 16, 32768) <= need
+        assert window_decode(d, B=B, window=4096, sinks=16, size=size(64, 128, 4096, 16, 32768)) == SMALL
