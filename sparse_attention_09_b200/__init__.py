@@ -5,7 +5,8 @@ sizes and the current CUDA stream to the C ABI declared in ``include/dsa.h`` and
 ``DSAError`` on a non-zero status.  The calls around the caches go through a small compiled module
 (``_marshal``) that also checks their tensors and raises ``ValueError``.  All computation happens in
 the library's CUDA kernels; there is no fallback.  Importing fails if the library has not been built
-(``python sparse_attention_09_b200/build.py``).
+(``python sparse_attention_09_b200/build.py``); without the module, which depends on the versions of torch and
+Python, the calls that use it do.
 """
 
 from __future__ import annotations
@@ -15,11 +16,31 @@ import os
 
 import torch
 
+from .build import marshal_current
+
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdsa.so")
 if not os.path.exists(_LIB_PATH):
     raise ImportError(f"libdsa.so is not built ({_LIB_PATH}); run: python sparse_attention_09_b200/build.py")
 _lib = ctypes.CDLL(_LIB_PATH)
-from . import _marshal  # noqa: E402  (after torch and the library, which it links)
+
+
+class _Unbuilt:
+    """In the compiled module's place when it cannot be loaded: the calls that need it say why, the others work."""
+
+    def __init__(self, why):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name}: _marshal.so {self.why}; run: python sparse_attention_09_b200/build.py")
+
+
+if not marshal_current():
+    _marshal = _Unbuilt("is not built for this torch and Python")
+else:
+    try:
+        from . import _marshal  # noqa: E402  (after torch and the library, which it links)
+    except ImportError as e:
+        _marshal = _Unbuilt(f"does not load ({e})")
 
 DSA_OK = 0
 DSA_ERR_INVALID_ARGUMENT = 1

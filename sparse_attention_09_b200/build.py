@@ -45,11 +45,29 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def marshal_target() -> str:
+    """What _marshal.so depends on beside its sources: the torch whose objects it reads, Python's and C++'s binary interface.
+    It is written into the module when it is compiled."""
+    import sysconfig
+
+    import torch
+
+    return f"dsa_marshal for torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}, cxx11 abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)};"
+
+
+def marshal_current() -> bool:
+    """Whether _marshal.so exists and was compiled for this torch and Python."""
+    if not os.path.exists(MARSHAL_PATH):
+        return False
+    with open(MARSHAL_PATH, "rb") as f:
+        return marshal_target().encode() in f.read()
+
+
 def _build_marshal(force: bool) -> None:
     """Compile _marshal.so against the libraries that torch loads (found by their names: torch is imported first)."""
     src = os.path.join(CSRC, "marshal.cpp")
     deps = [src, os.path.join(ROOT, "include", "dsa.h")]
-    if not force and os.path.exists(MARSHAL_PATH) and all(os.path.getmtime(d) <= os.path.getmtime(MARSHAL_PATH) for d in deps):
+    if not force and marshal_current() and all(os.path.getmtime(d) <= os.path.getmtime(MARSHAL_PATH) for d in deps):
         return
     import sysconfig
 
@@ -59,7 +77,7 @@ def _build_marshal(force: bool) -> None:
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = MARSHAL_PATH + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DDSA_MARSHAL_TARGET="{marshal_target()}"',
            "-isystem", os.path.join(base, "include"), "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"), src, "-o", tmp,
            "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",

@@ -19,6 +19,12 @@
 
 #include "../../include/dsa.h"
 
+#ifndef DSA_MARSHAL_TARGET
+#error "build.py says which torch and Python this module is compiled for"
+#endif
+// Read from the file by build.py and the package, which do not load a module made for another torch or Python.
+extern "C" __attribute__((used, visibility("default"))) const char dsa_marshal_target[] = DSA_MARSHAL_TARGET;
+
 namespace {
 
 // A message for ValueError.
