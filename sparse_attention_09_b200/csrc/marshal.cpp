@@ -2,9 +2,10 @@
 //
 // These calls take tensors whose types, shapes and strides the C ABI cannot see, and a decode step makes
 // several of them.  Checked and passed from Python a call took 8 to 11 us, of which 3 are the launch;
-// here the checks are a few hundred nanoseconds.  Every function takes its arguments by position and
-// returns the library's status, or raises ValueError for a tensor that it cannot pass on: of another
-// type, shape or layout, or on another device than the current one (whose stream the work goes to).
+// here the checks are a few hundred nanoseconds.  Python's lock is released for the call itself.  Every
+// function takes its arguments by position and returns the library's status, or raises ValueError for a
+// tensor that it cannot pass on: of another type, shape or layout, or on another device than the current
+// one (whose stream the work goes to).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -149,6 +150,17 @@ int32_t columns(const Args& a, int64_t n) {
   return static_cast<int32_t>(n);
 }
 
+// Calls the library without Python's lock, which the launch does not need: with a full launch queue it waits, and
+// what it waits for may itself need a Python thread.  The arguments are read before.
+template <typename... P, typename... A>
+dsa_status unlocked(dsa_status (*f)(P...), A... a) {
+  struct Released {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Released() { PyEval_RestoreThread(state); }
+  } released;
+  return f(a...);
+}
+
 template <typename F>
 PyObject* guarded(F f) {
   try {
@@ -178,10 +190,10 @@ PyObject* rmsnorm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const int64_t groups = (cols + DSA_QUANT_GROUP - 1) / DSA_QUANT_GROUP;
     float* sp = static_cast<float*>(grouped ? dense(a, 7, "scale", at::kFloat, {rows, groups}, dev)
                                             : dense(a, 7, "scale", at::kFloat, {rows}, dev));
-    return dsa_rmsnorm(xr.p, xr.ld, res.p, res.ld, dense(a, 1, "weight", type, {cols}, dev), rows, columns(a, cols), code,
-                       static_cast<float>(a.real(2)), y.p, y.ld, out.p, out.ld,
-                       static_cast<uint8_t*>(dense(a, 6, "codes", at::kByte, shape, dev)), sp, grouped ? DSA_QUANT_GROUP : 0,
-                       static_cast<float*>(dense(a, 8, "rstd", at::kFloat, {rows}, dev)), a.stream(9, dev));
+    return unlocked(dsa_rmsnorm, xr.p, xr.ld, res.p, res.ld, dense(a, 1, "weight", type, {cols}, dev), rows, columns(a, cols), code,
+                    static_cast<float>(a.real(2)), y.p, y.ld, out.p, out.ld,
+                    static_cast<uint8_t*>(dense(a, 6, "codes", at::kByte, shape, dev)), sp, grouped ? DSA_QUANT_GROUP : 0,
+                    static_cast<float*>(dense(a, 8, "rstd", at::kFloat, {rows}, dev)), a.stream(9, dev));
   });
 }
 
@@ -206,10 +218,10 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const Rows res = strided(a, 7, "dresidual", type, shape, dev), dh = strided(a, 4, "dh", type, shape, dev);
     size_t bytes;
     void* ws = workspace_of(a, 6, dev, &bytes);
-    return dsa_rmsnorm_backward(g.p, g.ld, h.p, h.ld, dense(a, 2, "weight", type, {cols}, dev),
-                                static_cast<float*>(dense(a, 3, "rstd", at::kFloat, {rows}, dev)), res.p, res.ld, rows,
-                                columns(a, cols), code, dh.p, dh.ld, static_cast<float*>(dense(a, 5, "dw", at::kFloat, {cols}, dev)),
-                                ws, bytes, a.stream(8, dev));
+    return unlocked(dsa_rmsnorm_backward, g.p, g.ld, h.p, h.ld, dense(a, 2, "weight", type, {cols}, dev),
+                    static_cast<float*>(dense(a, 3, "rstd", at::kFloat, {rows}, dev)), res.p, res.ld, rows,
+                    columns(a, cols), code, dh.p, dh.ld, static_cast<float*>(dense(a, 5, "dw", at::kFloat, {cols}, dev)),
+                    ws, bytes, a.stream(8, dev));
   });
 }
 
@@ -225,7 +237,7 @@ PyObject* rope(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const at::Tensor& out = a.required(3, "out");
     const Rows o = strided(a, 3, "out", x.scalar_type(), shape, dev);
     const int32_t rot = a.int32(5, "rot_dim");
-    return dsa_rope(xr.p, xr.ld, x.stride(1), o.p, o.ld, out.stride(1), shape[0], columns(a, shape[1]), columns(a, shape[2]),
+    return unlocked(dsa_rope, xr.p, xr.ld, x.stride(1), o.p, o.ld, out.stride(1), shape[0], columns(a, shape[1]), columns(a, shape[2]),
                     a.int32(4, "rot_offset"), rot, a.int32(6, "layout"), code,
                     static_cast<int32_t*>(dense(a, 1, "positions", at::kInt, {shape[0]}, dev)),
                     static_cast<double*>(dense(a, 2, "freqs", at::kDouble, {std::max<int64_t>(rot / 2, 0)}, dev)),
@@ -246,12 +258,12 @@ PyObject* cache_append(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const int64_t d_I = key != nullptr ? key->size(1) : 128;
     const Rows kv = strided(a, 0, "kv", at::kBFloat16, {rows, 576}, dev);
     const Rows k = strided(a, 3, "key", at::kBFloat16, {rows, d_I}, dev);
-    return dsa_cache_append(kv.p, kv.ld, dense(a, 1, "kv_weight", at::kBFloat16, {512}, dev), static_cast<float>(a.real(2)), k.p, k.ld,
-                            columns(a, d_I), static_cast<int32_t*>(dense(a, 4, "seq", at::kInt, {rows}, dev)),
-                            static_cast<int32_t*>(dense(a, 5, "positions", at::kInt, {rows}, dev)), rows, a.int32(9, "batch"),
-                            static_cast<double*>(dense(a, 6, "freqs", at::kDouble, {32}, dev)), static_cast<float>(a.real(13)),
-                            a.int32(10, "layout"), a.int32(11, "key_layout"), a.int32(12, "key_rot_offset"), a.desc(7), a.desc(8),
-                            a.stream(14, dev));
+    return unlocked(dsa_cache_append, kv.p, kv.ld, dense(a, 1, "kv_weight", at::kBFloat16, {512}, dev), static_cast<float>(a.real(2)), k.p, k.ld,
+                    columns(a, d_I), static_cast<int32_t*>(dense(a, 4, "seq", at::kInt, {rows}, dev)),
+                    static_cast<int32_t*>(dense(a, 5, "positions", at::kInt, {rows}, dev)), rows, a.int32(9, "batch"),
+                    static_cast<double*>(dense(a, 6, "freqs", at::kDouble, {32}, dev)), static_cast<float>(a.real(13)),
+                    a.int32(10, "layout"), a.int32(11, "key_layout"), a.int32(12, "key_rot_offset"), a.desc(7), a.desc(8),
+                    a.stream(14, dev));
   });
 }
 
@@ -284,8 +296,8 @@ PyObject* window_prefill(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (latent != nullptr && latent->kind == DSA_KV_CONTIGUOUS && w.q.size(0) != latent->total_tokens)
       throw Refusal("dsa_window_mla_prefill: q has " + std::to_string(w.q.size(0)) + " rows, latent " +
                     std::to_string(latent->total_tokens) + " tokens");
-    return dsa_window_mla_prefill(w.qp, latent, w.B, w.H, a.int32(4, "window"), a.int32(5, "sinks"), static_cast<float>(a.real(6)),
-                                  w.out, w.lse, a.stream(9, w.dev));
+    return unlocked(dsa_window_mla_prefill, w.qp, latent, w.B, w.H, a.int32(4, "window"), a.int32(5, "sinks"), static_cast<float>(a.real(6)),
+                    w.out, w.lse, a.stream(9, w.dev));
   });
 }
 
@@ -298,8 +310,8 @@ PyObject* window_decode(PyObject*, PyObject* const* v, Py_ssize_t n) {
       throw Refusal("dsa_window_mla_decode: q has " + std::to_string(w.q.size(0)) + " rows, B = " + std::to_string(w.B));
     size_t bytes;
     void* ws = workspace_of(a, 9, w.dev, &bytes);
-    return dsa_window_mla_decode(w.qp, a.desc(1), w.B, w.H, a.int32(4, "window"), a.int32(5, "sinks"), static_cast<float>(a.real(6)),
-                                 w.out, w.lse, ws, bytes, a.stream(10, w.dev));
+    return unlocked(dsa_window_mla_decode, w.qp, a.desc(1), w.B, w.H, a.int32(4, "window"), a.int32(5, "sinks"), static_cast<float>(a.real(6)),
+                    w.out, w.lse, ws, bytes, a.stream(10, w.dev));
   });
 }
 
