@@ -488,9 +488,9 @@ dsa_status dsa_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling, 
  * sequences share a page that is written: which row's values a slot named twice keeps is not defined.
  * Slots that no row names are not touched.  kv and key lie outside the caches.  rows == 0 is a no-op.
  * DSA_ERR_INVALID_ARGUMENT: NULL pointers, kv not 16-byte aligned or ld_kv no multiple of 8, key not
- * 4-byte aligned or ld_key odd, key_rot_offset odd or outside [0, d_I - 64], caches misaligned
- * (latent data 16 bytes, key data 2), inconsistent sizes; DSA_ERR_UNSUPPORTED: d_I not 64 or 128,
- * page size other than 64, rows or rows of a cache > 2^31 - 1.
+ * 4-byte aligned or ld_key odd (row strides count from two rows on), key_rot_offset odd or outside
+ * [0, d_I - 64], caches misaligned (latent data 16 bytes, key data 2), inconsistent sizes;
+ * DSA_ERR_UNSUPPORTED: d_I not 64 or 128, page size other than 64, rows or rows of a cache > 2^31 - 1.
  */
 dsa_status dsa_cache_append(const void* kv, int64_t ld_kv, const void* kv_weight, float eps, const void* key,
                             int64_t ld_key, int32_t d_I, const int32_t* seq, const int32_t* positions, int64_t rows,

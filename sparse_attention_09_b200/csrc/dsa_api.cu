@@ -1259,7 +1259,8 @@ dsa_status dsa_cache_append(const void* kv, int64_t ld_kv, const void* kv_weight
   AppendParams p;
   std::memset(&p, 0, sizeof(p));
   if (latent != nullptr) {
-    if (kv_weight == nullptr || !aligned(kv, 16) || !aligned(kv_weight, 16) || ld_kv % 8 != 0 || (rows > 1 && ld_kv < kLatentDim))
+    if (kv_weight == nullptr || !aligned(kv, 16) || !aligned(kv_weight, 16) ||
+        (rows > 1 && (ld_kv % 8 != 0 || ld_kv < kLatentDim)))
       return DSA_ERR_INVALID_ARGUMENT;
     if (!(eps >= 0.f) || !std::isfinite(eps) || (layout != DSA_ROPE_INTERLEAVED && layout != DSA_ROPE_HALF))
       return DSA_ERR_INVALID_ARGUMENT;
@@ -1268,7 +1269,7 @@ dsa_status dsa_cache_append(const void* kv, int64_t ld_kv, const void* kv_weight
   }
   if (keys != nullptr) {
     if (d_I != 64 && d_I != 128) return DSA_ERR_UNSUPPORTED;
-    if (!aligned(key, 4) || ld_key % 2 != 0 || (rows > 1 && ld_key < d_I)) return DSA_ERR_INVALID_ARGUMENT;
+    if (!aligned(key, 4) || (rows > 1 && (ld_key % 2 != 0 || ld_key < d_I))) return DSA_ERR_INVALID_ARGUMENT;
     if (key_layout != DSA_ROPE_INTERLEAVED && key_layout != DSA_ROPE_HALF) return DSA_ERR_INVALID_ARGUMENT;
     if (key_rot_offset < 0 || key_rot_offset > d_I - 64 || key_rot_offset % 2 != 0) return DSA_ERR_INVALID_ARGUMENT;
     const dsa_status st = append_cache(keys, true, 2, &p.keys);

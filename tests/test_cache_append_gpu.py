@@ -219,3 +219,20 @@ def test_wrapper_refusals():
         with pytest.raises(dsa.DSAError):
             dsa.dsa_cache_append(**{**ok, **kw})
     assert (c.latent == 7).all()
+
+
+def test_the_stride_of_a_single_row_does_not_matter():
+    c = Caches(2, 2, 128)
+    kv, key, w = rnd((1, 577), 1)[:, :576], rnd((1, 129), 2)[:, :128], rnd((512,), 3)
+    assert kv.stride(0) == 577 and key.stride(0) == 129
+    pos, freqs = torch.tensor([70], dtype=torch.int32), dsa.dsa_rope_frequencies(64, 10000.0)[0].cuda()
+    dsa.dsa_cache_append(kv, w, EPS, key, torch.ones(1, dtype=torch.int32, device="cuda"), pos.cuda(), freqs, c.lat_desc, c.key_desc)
+    assert dsa.dsa_device_error() == 0
+    check(c.latent.flatten(0, 1), c.codes.flatten(0, 1), c.scale.flatten(), c.slots([1], pos), kv, w, key, pos.numpy(), freqs, False,
+          True, 0, 1.0)
+    many_kv, many_key = rnd((2, 577), 1)[:, :576], rnd((2, 129), 2)[:, :128]  # of two rows it does
+    pos2, seq2 = torch.tensor([3, 4], dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    for kw in ((many_kv, None), (None, many_key)):
+        with pytest.raises(dsa.DSAError):
+            dsa.dsa_cache_append(kw[0], w if kw[0] is not None else None, EPS, kw[1], seq2, pos2, freqs,
+                                 c.lat_desc if kw[0] is not None else None, c.key_desc if kw[1] is not None else None)
