@@ -431,6 +431,14 @@ def _cache(where, name, desc, dtype, width, dev):
     desc._checked = (dtype, width, dev)
 
 
+def _integer(where, name, value, bits=32):
+    """An argument of the library as an integer of this size; ctypes would cut what does not fit."""
+    value = int(value)
+    if not -2 ** (bits - 1) <= value < 2 ** (bits - 1):
+        raise ValueError(f"{where}: {name} does not fit {bits} bits")
+    return value
+
+
 def _handle(stream):
     return None if stream is None else stream.cuda_stream
 
@@ -445,7 +453,8 @@ def dsa_rmsnorm(x, weight, eps, y=None, residual=None, residual_out=None, codes=
 
 
 def dsa_rmsnorm_backward_workspace_size(rows, cols) -> int:
-    return int(_lib.dsa_rmsnorm_backward_workspace_size(int(rows), int(cols)))
+    w = "dsa_rmsnorm_backward_workspace_size"
+    return int(_lib.dsa_rmsnorm_backward_workspace_size(_integer(w, "rows", rows, 64), _integer(w, "cols", cols)))
 
 
 def dsa_rmsnorm_backward(dy, h, weight, rstd, dh, dw, workspace, dresidual=None, stream=None):
@@ -468,9 +477,10 @@ def dsa_rope(x, positions, freqs, out, rot_offset, rot_dim, layout=DSA_ROPE_INTE
 def dsa_rope_frequencies(rot_dim, theta, scaling=DSA_ROPE_PLAIN, factor=1.0, original_ctx=0.0, beta_fast=32.0, beta_slow=1.0):
     """(freqs, mscale): the float64 CPU tensor [rot_dim / 2] of radians per position, plain or scaled
     for a context `factor` times original_ctx, and the factor on the rotated values (host only)."""
-    freqs = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float64)
+    rot_dim, scaling = (_integer("dsa_rope_frequencies", n, v) for n, v in (("rot_dim", rot_dim), ("scaling", scaling)))
+    freqs = torch.empty(max(rot_dim // 2, 1), dtype=torch.float64)
     mscale = _F32(1.0)
-    _check(_lib.dsa_rope_frequencies(int(rot_dim), float(theta), int(scaling), float(factor), float(original_ctx),
+    _check(_lib.dsa_rope_frequencies(rot_dim, float(theta), scaling, float(factor), float(original_ctx),
                                      float(beta_fast), float(beta_slow), freqs.data_ptr(), ctypes.byref(mscale)),
            "dsa_rope_frequencies")
     return freqs, float(mscale.value)
@@ -511,14 +521,18 @@ def dsa_window_mla_prefill(q, latent: Desc, B, H, window, sinks, sm_scale, out, 
     return out
 
 
+def _window_sizes(where, *sizes):
+    return [_integer(where, n, v) for n, v in zip(("B", "H", "window", "sinks", "max_ctx"), sizes)]
+
+
 def dsa_window_mla_workspace_size(B, H, window, sinks, max_ctx) -> int:
     """Bytes for one dsa_window_mla_decode call; a smaller batch can need more (see dsa_window_mla_workspace_limit)."""
-    return int(_lib.dsa_window_mla_workspace_size(int(B), int(H), int(window), int(sinks), int(max_ctx)))
+    return int(_lib.dsa_window_mla_workspace_size(*_window_sizes("dsa_window_mla_workspace_size", B, H, window, sinks, max_ctx)))
 
 
 def dsa_window_mla_workspace_limit(B, H, window, sinks, max_ctx) -> int:
     """Bytes for every dsa_window_mla_decode call with at most these sequences, heads, window, sinks and context."""
-    return int(_lib.dsa_window_mla_workspace_limit(int(B), int(H), int(window), int(sinks), int(max_ctx)))
+    return int(_lib.dsa_window_mla_workspace_limit(*_window_sizes("dsa_window_mla_workspace_limit", B, H, window, sinks, max_ctx)))
 
 
 def dsa_window_mla_decode(q, latent: Desc, B, H, window, sinks, sm_scale, out, lse=None, workspace=None, stream=None):

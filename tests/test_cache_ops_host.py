@@ -311,3 +311,21 @@ def test_window_workspace_limit_serves_smaller_batches():
     for B in (1, 2, 40, 48):
         assert 0 < size(B, 128, 4096, 16, 32768) <= need
         assert window_decode(d, B=B, window=4096, sinks=16, size=size(64, 128, 4096, 16, 32768)) == SMALL
+
+
+def test_sizes_beyond_their_integers_are_refused_and_not_cut():
+    """A window of 2^31 for "everything" was cut to a negative one, for which no workspace is needed."""
+    for f in (dsa.dsa_window_mla_workspace_size, dsa.dsa_window_mla_workspace_limit):
+        assert f(3, 128, 2 ** 31 - 1, 0, 131072) > 0
+        for args in ((3, 128, 2 ** 31, 0, 131072), (3, 128, 4096, 2 ** 32, 131072), (2 ** 32 + 3, 128, 4096, 0, 131072), (3, -2 ** 31 - 1, 4096, 0, 1),
+                     (3, 128, 4096, 0, 2 ** 32 + 131072)):
+            with pytest.raises(ValueError, match="32 bits"):
+                f(*args)
+    for args in ((4, 2 ** 32 + 64), (4, -2 ** 31 - 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            dsa.dsa_rmsnorm_backward_workspace_size(*args)
+    with pytest.raises(ValueError, match="64 bits"):
+        dsa.dsa_rmsnorm_backward_workspace_size(2 ** 64 + 4, 64)
+    for args in ((-2 ** 32 + 64, 1e4), (64, 1e4, 2 ** 32)):  # the table of 2^31 and more dims itself is not asked for here
+        with pytest.raises(ValueError, match="32 bits"):
+            dsa.dsa_rope_frequencies(*args)
