@@ -95,10 +95,9 @@ static_assert(kOffKQ + kGroups * kGroupBytes == kOffV, "one chunk of own rows");
 // What a query costs beside its chunks (its Q, the pipeline's fill, the readout of O), in chunks:
 // measured 3 to 4 us against 1.7 to 1.9 per chunk (1 and 3 share as evenly).
 constexpr int kUnitCost = 2;
-// Decode: pages are brought into L2 this many chunks ahead of their copies (one sequence of 128K 54.5 / 57.0 /
-// 62.6 us with 1 / 2 / 4, three up to 128K 78 / 79.5 / 88).
+// Decode: pages are brought into L2 this many chunks ahead of their copies.  Fitted on shared-out sequences only
+// (one of 128K 54.5 / 57.0 / 62.6 us with 1 / 2 / 4, three up to 128K 78 / 79.5 / 88), used for whole ones too.
 constexpr int kAhead = 1;
-constexpr int kMinShare = 1;  // chunks that a cluster takes at least when sequences are split
 
 // The entries of a query that has `len` keys up to its own: entry e < ns is position e, a later one
 // below `end` position e + shift.
@@ -190,8 +189,7 @@ __device__ __forceinline__ void plan_walk(const WinParams& p, int cid, int ncl, 
   for (int b = lane; b < p.B; b += 32) total += visible(p, context_of(p, b)).chunks() + kUnitCost;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  // not more clusters than give each a whole sequence or kMinShare chunks
-  const int n = static_cast<int>(min(static_cast<int64_t>(ncl), max(static_cast<int64_t>(p.B), total / kMinShare)));
+  const int n = static_cast<int>(min(static_cast<int64_t>(ncl), total));  // clusters: each has a cost unit at least
   out.lo = cid < n ? total * cid / n : total;
   out.hi = cid < n ? total * (cid + 1) / n : total;
   out.u = p.B;
