@@ -11,7 +11,7 @@
 // what is the same for all lanes costs as much to compute as what is not.  So a warp takes tokens
 // in blocks of 32: lane j finds the slots of the block's token j, and the rows of the next three
 // tokens are always on their way into a ring of the warp's own in shared memory (asynchronous
-// copies).  Measured on 65536 tokens, d_I = 128: 48.9 us with a token's loads issued together and
+// copies).  Measured on the device alone, 65536 tokens, d_I = 128: 48.9 us with a token's loads issued together and
 // no look-ahead, 41.3 us with the ring and each token's slots found by all lanes, 33.2 us with both
 // (5.3 TB/s, 0.81 of measured HBM).
 #pragma once

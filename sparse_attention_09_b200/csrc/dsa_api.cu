@@ -248,8 +248,8 @@ dsa_status launch_mla_pair(const void* latent, const void* q, int64_t q_rows, co
 // sequences) instead of giving each cluster whole sequences.  In chunks' times: whole sequences take
 // rounds of (chunks + kUnitCost); shared, the even share, an eighth of it and 8 for what splits add (a
 // second piece of work per cluster, fp32 partial outputs, the merge).  By the longest context the
-// arguments allow: the contexts themselves are on the device.
-// Measured (us, shared / whole): 8 sequences of 512 keys 16.0 / 16.1; of 1024 keys 8: 18.6 / 23.3, 24:
+// arguments allow: the contexts themselves are on the device, so a batch far below it pays for the sharing.
+// Measured (us on the device, contexts at the longest, shared / whole): 8 sequences of 512 keys 16.0 / 16.1; of 1024 keys 8: 18.6 / 23.3, 24:
 // 24.8 / 23.7; of 2048 keys 16: 25 / 38, 40: 46 / 40, 96: 85 / 87; of 4096 keys 48: 78 / 81, 64: 101 / 87, 112: 162 / 178,
 // 128: 187 / 185; of 8192 keys 56: 149 / 182, 64: 189 / 180.
 constexpr int kShareSeqs = 1024;  // a cluster's start is found by a scan of the contexts
@@ -283,6 +283,7 @@ dsa_status launch_window(const void* latent, const void* q, const WinParams& p, 
 bool mla_shape_ok(int H, int k) { return H >= 1 && H <= 128 && k >= 64 && k <= 2048 && k % 64 == 0; }
 
 // ---- row operators: norm, rotary positions, cache append ---------------------------------------
+// Times here are of the device alone, calls back to back on one set of buffers (of which L2 keeps a part).
 constexpr int kSms = 148;
 constexpr int kMostCols = 1 << 30;  // columns of a row: the kernels' column numbers, a step past the row's end, fit an int
 
@@ -438,6 +439,8 @@ dsa_status launch_rmsnorm_backward(const NormBwdParams& p, int piece, float* dw,
     rmsnorm_backward_ring_kernel<T><<<static_cast<unsigned>(ctas), row_threads(p.cols, 8, 1), smem, s>>>(p, stages);
     return launch_dw(p, ctas, dw, s);
   }
+  // beyond the ring: registers for two pieces of three operands and the row ahead, with spills at 1024 threads (8192 x
+  // 12288 bf16 with the residual's gradient 262 us, 0.47 of measured HBM; x 16384 299, 0.55; x 12288 fp32 661, 0.37)
   if (n <= 2 * 1024) return launch_rmsnorm_backward_v<T, 8, 2, 0>(p, dw, s);
   rmsnorm_backward_general_kernel<T><<<static_cast<unsigned>(ctas), norm::kGeneralThreads, 0, s>>>(p);
   return launch_dw(p, ctas, dw, s);

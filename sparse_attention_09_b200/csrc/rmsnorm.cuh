@@ -11,9 +11,9 @@
 // pieces smaller than 8), to one warp or a half or quarter of one (no block barrier).  Rows that are not made of aligned pieces of 8
 // elements use the same kernels with pieces of 4, 2 or 1.  Rows too wide for the registers of a CTA take
 // the general kernels, which read a row again for each pass (from L1 / L2).
-// Measured on 32768 x 4096 bf16 with residual, y and codes: 180 us (6.7 TB/s, 1.02 of measured HBM's copy
-// rate; 193 us with a division per code, 185 with 2 pieces per thread); 65536 x 128 bf16 9.3 us (half a
-// warp per row; a warp, half of it idle: 14.9).
+// Measured on the device alone (calls in a captured graph): 32768 x 4096 bf16 with residual, y and codes 180 us
+// (6.7 TB/s, 1.02 of measured HBM's copy rate; 200 a call among others, from Python; 193 us with a division per code, 185 with
+// 2 pieces per thread); 65536 x 128 bf16 9.3 us on one set of buffers (half a warp per row; a warp, half of it idle: 14.9).
 #pragma once
 
 #include "elem.cuh"
@@ -424,9 +424,9 @@ __global__ void __launch_bounds__(LANES > 0 ? norm::kWarps * 32 : 1024) rmsnorm_
 // Backward for CTA-wide rows of whole 8-element pieces: one piece per thread, and the rows (dy, h and
 // the residual's gradient) come through a ring of shared-memory stages filled by bulk copies, several
 // rows ahead, so that the bytes in flight do not depend on registers or on the reduction's barrier.
-// Measured on 16384 x 5120 bf16 with the residual's gradient: 129 us with one row ahead in
-// registers (above), 109.9 us with the ring (6.1 TB/s, 0.93 of measured HBM); 128 us while rstd was not
-// read a row ahead too.
+// Measured on the device alone, 16384 x 5120 bf16 with the residual's gradient: 129 us with one row ahead in
+// registers (above), 109.9 us with the ring (6.1 TB/s, 0.93 of measured HBM; 120 a call among others, from Python); 128 us while
+// rstd was not read a row ahead too.
 template <typename T>
 __global__ void __launch_bounds__(1024) rmsnorm_backward_ring_kernel(const NormBwdParams p, int stages) {
   using elem::Raw8;

@@ -15,9 +15,9 @@
 // a thread's piece, and its place in the cos / sin table, stay the same for all the (row, head)
 // pairs that its group walks through.  The loads of the first batch are issued before the table of
 // the CTA's rows is made (it serves every head of a row).
-// Measured: 16384 x 64 heads x 128 bf16, half layout, 94.2 us (5.7 TB/s, 0.87 of measured HBM; 122 us with
-// items dealt out singly and sincospif); 6001 x 64 x 128 fp32 62.9 us (0.95); 12000 x 64 x 128 bf16 with 6
-// rotated dims 88.6 us (0.68; 354 us by pairs and single elements alone).
+// Measured on the device alone: 16384 x 64 heads x 128 bf16, half layout, 94.2 us (5.7 TB/s, 0.87 of measured HBM; 100 a
+// call among others, from Python; 122 us with items dealt out singly and sincospif); 6001 x 64 x 128 fp32 62.9 us (0.95);
+// 12000 x 64 x 128 bf16 with 6 rotated dims 85 to 89 us (0.68 to 0.71; 354 us by pairs and single elements alone).
 #pragma once
 
 #include "elem.cuh"

@@ -93,7 +93,8 @@ constexpr int kGroupBytes = kGroupBlocks * kKQBlockBytes;
 static_assert(kOffKQ + kGroups * kGroupBytes == kOffV, "one chunk of own rows");
 
 // What a query costs beside its chunks (its Q, the pipeline's fill, the readout of O), in chunks:
-// measured 3 to 4 us against 1.7 to 1.9 per chunk (1 and 3 share as evenly).
+// measured 3 to 4 us against 1.7 to 1.9 per chunk in prefill (1 and 3 share as evenly; decode's chunks take 2.0 with
+// the pages in L2, 2.25 without).
 constexpr int kUnitCost = 2;
 // Decode: pages are brought into L2 this many chunks ahead of their copies.  Fitted on shared-out sequences only
 // (one of 128K 54.5 / 57.0 / 62.6 us with 1 / 2 / 4, three up to 128K 78 / 79.5 / 88), used for whole ones too.
