@@ -406,8 +406,11 @@ def dsa_row_partition(L, k, parts, indexer_cost, mla_cost):
 
 def _cache(where, name, desc, dtype, width, dev):
     """Checks the tensors of a descriptor once for this row type, width and device."""
-    if desc._checked == (dtype, width, dev):
-        return
+    try:
+        if desc._checked == (dtype, width, dev):
+            return
+    except AttributeError:
+        raise ValueError(f"{where}: {name} must be a descriptor of a cache (paged_desc, contiguous_desc)") from None
     data, scale, *tables = desc._refs
     if data.dtype is not dtype or data.shape[-1] != width:
         raise ValueError(f"{where}: {name} must describe {dtype} rows of {width}, got {data.dtype} {tuple(data.shape)}")
@@ -429,6 +432,13 @@ def _cache(where, name, desc, dtype, width, dev):
     if any(t.dtype is not torch.int32 for t in tables):
         raise ValueError(f"{where}: the tables and lengths that {name} describes must be int32")
     desc._checked = (dtype, width, dev)
+
+
+def _device(where, name, t):
+    try:
+        return t.get_device()
+    except AttributeError:
+        raise ValueError(f"{where}: {name} must be a tensor") from None
 
 
 def _integer(where, name, value, bits=32):
@@ -493,21 +503,23 @@ def dsa_cache_append(kv, kv_weight, eps, key, seq, positions, freqs, latent: Des
     position positions[r] of sequence seq[r] (seq None: sequence r; -1: skipped) of the caches that
     latent and keys describe.  kv, kv_weight and latent, or key and keys, may be None."""
     w = "dsa_cache_append"
-    dev = positions.get_device()
+    dev = _device(w, "positions", positions)
     if latent is not None:
         _cache(w, "latent", latent, torch.bfloat16, 576, dev)
     if keys is not None:
+        if key is not None:
+            _device(w, "key", key)
         _cache(w, "keys", keys, torch.uint8, 128 if key is None else key.shape[-1], dev)
         if latent is not None and latent.batch != keys.batch:
             raise ValueError(f"{w}: latent describes {latent.batch} sequences, keys {keys.batch}")
-    some = latent or keys
+    some = latent if latent is not None else keys
     _check(_marshal.cache_append(kv, kv_weight, eps, key, seq, positions, freqs, latent and latent._address,
                                  keys and keys._address, some.batch if some else 0, layout, key_layout, key_rot_offset, mscale,
                                  _handle(stream)), w)
 
 
 def _windowed(w, q, latent, B):
-    _cache(w, "latent", latent, torch.bfloat16, 576, q.get_device())
+    _cache(w, "latent", latent, torch.bfloat16, 576, _device(w, "q", q))
     if latent.batch != B:
         raise ValueError(f"{w}: latent describes {latent.batch} sequences, B = {B}")
     return latent._address

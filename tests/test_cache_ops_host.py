@@ -329,3 +329,23 @@ def test_sizes_beyond_their_integers_are_refused_and_not_cut():
     for args in ((-2 ** 32 + 64, 1e4), (64, 1e4, 2 ** 32)):  # the table of 2^31 and more dims itself is not asked for here
         with pytest.raises(ValueError, match="32 bits"):
             dsa.dsa_rope_frequencies(*args)
+
+
+def test_wrappers_refuse_what_is_no_descriptor_or_tensor_by_value_error():
+    q, out, pos = torch.zeros(2, 16, 576, dtype=torch.bfloat16), torch.zeros(2, 16, 512, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    lat = dsa.contiguous_desc(torch.zeros(2, 576, dtype=torch.bfloat16), torch.tensor([0, 2], dtype=torch.int32), 2)
+    for call in (dsa.dsa_window_mla_prefill, dsa.dsa_window_mla_decode):
+        for desc in (None, q, lat.struct):
+            with pytest.raises(ValueError, match="latent must be"):
+                call(q, desc, 1, 16, 8, 0, 0.04, out)
+        with pytest.raises(ValueError, match="q must be a tensor"):
+            call(None, lat, 1, 16, 8, 0, 0.04, out)
+    for bad in (q, lat.struct, 3):
+        with pytest.raises(ValueError, match="latent must be"):
+            dsa.dsa_cache_append(q, None, 0.0, None, None, pos, None, bad, None)
+        with pytest.raises(ValueError, match="keys must be"):
+            dsa.dsa_cache_append(None, None, 0.0, pos, None, pos, None, None, bad)
+    with pytest.raises(ValueError, match="positions must be a tensor"):
+        dsa.dsa_cache_append(None, None, 0.0, None, None, None, None, lat, None)
+    with pytest.raises(ValueError, match="key must be a tensor"):
+        dsa.dsa_cache_append(None, None, 0.0, [1.0], None, pos, None, None, lat)
